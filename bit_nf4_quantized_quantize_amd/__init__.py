@@ -3,7 +3,9 @@
 NF4 blockwise quantisation with double quantisation, dequantisation, and the
 forward/backward of a linear layer with a LoRA adapter over the frozen NF4
 weight, as hand-written HIP kernels behind the C ABI of include/qlora_nf4.h.
-`binding` is the ctypes layer over that ABI; `build` compiles the library.
+`binding` is the ctypes layer over that ABI; `decoder` the one over
+include/qlora_decoder.h (norms and residual, rotary positions, paged decoding);
+`build` compiles the library.
 """
 
 from .binding import (  # noqa: F401
@@ -19,4 +21,15 @@ from .binding import (  # noqa: F401
     qlora_nf4_quantize,
     qlora_nf4_quantize_workspace,
     qlora_nf4_storage_bytes,
+)
+from .decoder import (  # noqa: F401
+    NormGrads,
+    PagedPlan,
+    RopeTable,
+    qlora_norm_residual_bwd,
+    qlora_norm_residual_fwd,
+    qlora_paged_attention,
+    qlora_paged_plan,
+    qlora_rope,
+    qlora_rope_cache_write,
 )

@@ -16,8 +16,9 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqlora_nf4.so")
 
-SOURCES = ["quantize.hip", "linear.hip", "optim.hip", "dropout.hip", "noalloc.hip", "probe.hip", "host.cpp", "abi.cpp"]
-HEADERS = ["device.h", "launch.h", "codebooks.h"]
+SOURCES = ["quantize.hip", "linear.hip", "optim.hip", "dropout.hip", "noalloc.hip", "probe.hip", "norm.hip", "rope.hip", "paged.hip",
+           "host.cpp", "abi.cpp", "decoder_abi.cpp"]
+HEADERS = ["device.h", "launch.h", "codebooks.h", "decoder.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

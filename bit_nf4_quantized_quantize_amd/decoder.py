@@ -1,0 +1,378 @@
+"""Thin ctypes binding of the decoder-block operators (include/qlora_decoder.h)
+in libqlora_nf4.so: the residual update with its norms, rotary positions, and
+decoding from a paged key-value cache.
+
+As in `binding`: argument marshalling only, functions carry the names of the C
+entry points, and a missing library raises.  All tensors of a call must be on
+one device, which need not be the current one.  Work runs on the current
+stream of that device, or on `stream`; outputs and workspaces a call allocates
+belong to the stream it runs on, and tensors it is given are marked as used
+there, so their memory is not handed out again before the call has run.
+"""
+
+import collections
+import ctypes
+import math
+
+import torch
+
+from . import binding as B
+
+_vp, _i64, _i32, _f32, _f64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_double
+
+NORM_MAX_WIDTH = 16384
+PLAN_MAX_SEQS = 4096
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+# Every function declared in include/qlora_decoder.h.
+EXPORTED = (
+    "qlora_norm_residual_fwd", "qlora_norm_residual_bwd_workspace", "qlora_norm_residual_bwd",
+    "qlora_rope_frequencies", "qlora_rope", "qlora_rope_cache_write", "qlora_paged_plan",
+    "qlora_paged_attention_workspace", "qlora_paged_attention",
+)
+
+_SIG = {
+    "qlora_norm_residual_fwd": [_vp, _i32, _vp, _i32, _i64, _i64, _vp, _vp, _f32, _vp, _f32, _vp, _vp, _vp],
+    "qlora_norm_residual_bwd_workspace": [_i64, _i64, _i32, _i32, _i32, ctypes.POINTER(_i64)],
+    "qlora_norm_residual_bwd": [_vp, _vp, _i32, _vp, _vp, _i32, _i64, _i64, _vp, _vp, _f32, _vp, _f32, _vp, _vp, _vp,
+                                _vp, _vp, _vp, _i64, _vp],
+    "qlora_rope_frequencies": [_i32, _f64, _i32, _f64, _f64, _f64, _f64, ctypes.POINTER(_f64), ctypes.POINTER(_f32)],
+    "qlora_rope": [_vp, _i64, _i32, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _f32,
+                   _i32, _i32, _vp],
+    "qlora_rope_cache_write": [_vp, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _i32, _i32, _vp, _vp,
+                               _f32, _i32, _vp, _vp, _vp, _i64, _i32, _vp],
+    "qlora_paged_plan": [_vp, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp],
+    "qlora_paged_attention_workspace": [_i64, _i32, _i32, _i32, _i64, _i32, ctypes.POINTER(_i64)],
+    "qlora_paged_attention": [_vp, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _i64, _i32, _vp, _i64, _vp, _f32, _vp, _vp,
+                              _vp, _i64, _vp],
+}
+
+_lib = None
+_DTYPES = {torch.float32: B.QLORA_DTYPE_F32, torch.bfloat16: B.QLORA_DTYPE_BF16}
+
+
+def lib():
+    """The loaded library with this header's functions declared."""
+    global _lib
+    if _lib is None:
+        L = B.lib()
+        for name, args in _SIG.items():
+            f = getattr(L, name)
+            f.restype, f.argtypes = _i32, args
+        _lib = L
+    return _lib
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+class _On:
+    """Makes the device of `tensors` and `stream` (if given) current; .stream
+    is the handle to launch on."""
+
+    __slots__ = ("stream", "_guards")
+
+    def __init__(self, stream, *tensors):
+        dev = None
+        for t in tensors:
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise ValueError("qlora_nf4 tensors must live on a HIP device")
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError("all tensors of a call must be on one device")
+        self._guards = ()
+        if stream is None:
+            if dev.index != torch.cuda.current_device():
+                self._guards = (torch.cuda.device(dev),)
+            stream = torch.cuda.current_stream(dev)
+        elif stream != torch.cuda.current_stream(dev):
+            if stream.device != dev:
+                raise ValueError("stream must belong to the tensors' device")
+            self._guards = (torch.cuda.stream(stream),)
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+        elif dev.index != torch.cuda.current_device():
+            self._guards = (torch.cuda.device(dev),)
+        self.stream = stream.cuda_stream
+
+    def __enter__(self):
+        for g in self._guards:
+            g.__enter__()
+        return self
+
+    def __exit__(self, *e):
+        for g in self._guards:
+            g.__exit__(*e)
+
+
+def _dense(t, name, shape, dtypes):
+    if t.dtype not in dtypes or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} and type "
+                         f"{' or '.join(str(d) for d in dtypes)}")
+
+
+def _gain(t, name, D):
+    if t is not None:
+        _dense(t, name, (D,), (torch.float32,))
+
+
+def _call(name, *args):
+    B._check(getattr(_lib or lib(), name)(*args), name)
+
+
+# --------------------------------------------------- norm, gate and residual
+
+def qlora_norm_residual_fwd(x, h=None, w_pre=None, w_post=None, gate=None, alpha=1.0, eps=1e-6, n_dtype=None, xo=None,
+                            n=None, stream=None):
+    """The step between two branches: xo = x + alpha * gate * norm(h) w_post,
+    n = norm(xo) w_pre (rms norms over the last dimension).  x [..., D] float32
+    or bfloat16; h (or None) of x's shape, bfloat16 or x's type; gains and gate
+    float32 [D] or None.  Returns (xo, n): xo is x when h is None, n is None
+    without w_pre and has h's type (n_dtype, or x's, without h).  xo may be
+    given as x itself: the stream is then updated in place."""
+    D = x.shape[-1]
+    T = x.numel() // D if D else 0
+    _dense(x, "x", x.shape, _DTYPES)
+    if h is not None:
+        _dense(h, "h", x.shape, _DTYPES)
+        nd = h.dtype
+        if n_dtype is not None and n_dtype != nd:
+            raise ValueError("n has the type of h")
+    else:
+        nd = n_dtype if n_dtype is not None else x.dtype
+        if nd not in _DTYPES:
+            raise ValueError("n_dtype must be torch.float32 or torch.bfloat16")
+    _gain(w_pre, "w_pre", D)
+    _gain(w_post, "w_post", D)
+    _gain(gate, "gate", D)
+    with _On(stream, x, h, w_pre, w_post, gate, xo, n) as on:
+        if xo is not None:
+            _dense(xo, "xo", x.shape, (x.dtype,))
+        elif h is not None:
+            xo = torch.empty_like(x)
+        if n is not None:
+            _dense(n, "n", x.shape, (nd,))
+        elif w_pre is not None:
+            n = torch.empty_like(x, dtype=nd)
+        _call("qlora_norm_residual_fwd", x.data_ptr(), _DTYPES[x.dtype], _ptr(h), _DTYPES[nd], T, D, _ptr(w_post),
+              _ptr(gate), alpha, _ptr(w_pre), eps, _ptr(xo), _ptr(n), on.stream)
+    return (x if xo is None else xo), n
+
+
+NormGrads = collections.namedtuple("NormGrads", "dx dh dw_pre dw_post dgate")
+
+
+def qlora_norm_residual_bwd(dxo, dn, xo, h=None, w_pre=None, w_post=None, gate=None, alpha=1.0, eps=1e-6,
+                            need_dh=True, need_gains=False, dx=None, dh=None, stream=None):
+    """Gradients of qlora_norm_residual_fwd: dxo, dn (either may be None) the
+    gradients of its outputs, xo the stream it returned, h its branch (needed
+    for w_post and the gradient of the gate).  Returns NormGrads: dx, dh (None
+    without need_dh) and, with need_gains, the float32 gradients of the gains
+    and the gate that the forward had."""
+    D = xo.shape[-1]
+    T = xo.numel() // D if D else 0
+    _dense(xo, "xo", xo.shape, _DTYPES)
+    hd = next((t.dtype for t in (h, dn, dh) if t is not None), xo.dtype)
+    for t, name, dt in ((dxo, "dxo", xo.dtype), (dx, "dx", xo.dtype), (dn, "dn", hd), (h, "h", hd), (dh, "dh", hd)):
+        if t is not None:
+            _dense(t, name, xo.shape, (dt,) if dt in _DTYPES else _DTYPES)
+    _gain(w_pre, "w_pre", D)
+    _gain(w_post, "w_post", D)
+    _gain(gate, "gate", D)
+    with _On(stream, xo, dxo, dn, h, w_pre, w_post, gate, dx, dh) as on:
+        dx = torch.empty_like(xo) if dx is None else dx
+        if dh is None and need_dh:
+            dh = torch.empty_like(xo, dtype=hd)
+        new = lambda: torch.empty(D, dtype=torch.float32, device=xo.device)  # noqa: E731
+        dw_pre = new() if need_gains and dn is not None else None
+        dw_post = new() if need_gains and w_post is not None else None
+        dgate = new() if need_gains and gate is not None else None
+        ws, nws = None, _i64(0)
+        if dw_pre is not None or dw_post is not None or dgate is not None:
+            _call("qlora_norm_residual_bwd_workspace", T, D, _DTYPES[xo.dtype], _DTYPES[hd], 3, ctypes.byref(nws))
+            ws = torch.empty(max(nws.value, 16), dtype=torch.uint8, device=xo.device)
+        _call("qlora_norm_residual_bwd", _ptr(dxo), xo.data_ptr(), _DTYPES[xo.dtype], _ptr(dn), _ptr(h), _DTYPES[hd],
+              T, D, _ptr(w_post), _ptr(gate), alpha, _ptr(w_pre), eps, dx.data_ptr(), _ptr(dh), _ptr(dw_post),
+              _ptr(dgate), _ptr(dw_pre), _ptr(ws), nws.value, on.stream)
+    return NormGrads(dx, dh, dw_pre, dw_post, dgate)
+
+
+# ---------------------------------------------------------- rotary positions
+
+def qlora_rope_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, original_len=0, beta_fast=32.0,
+                           beta_slow=1.0):
+    """(turns per position of each pair as a list of rot_dim / 2 floats, factor
+    of the rotated values); see qlora_rope_scaling for `scaling`."""
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {', '.join(ROPE_SCALING)}")
+    turns, m = (_f64 * max(rot_dim // 2, 1))(), _f32(0.0)
+    lib()
+    _call("qlora_rope_frequencies", rot_dim, base, ROPE_SCALING[scaling], factor, original_len, beta_fast, beta_slow,
+          turns, ctypes.byref(m))
+    return list(turns), m.value
+
+
+class RopeTable:
+    """The frequencies of rotary positions on a device, built once per model:
+    `turns` (float64 [rot_dim / 2]), `mscale`, and the pair layout."""
+
+    def __init__(self, rot_dim, base=10000.0, scaling="none", factor=1.0, original_len=0, beta_fast=32.0,
+                 beta_slow=1.0, interleaved=False, device=None):
+        turns, self.mscale = qlora_rope_frequencies(rot_dim, base, scaling, factor, original_len, beta_fast,
+                                                    beta_slow)
+        self.rot_dim, self.interleaved = int(rot_dim), bool(interleaved)
+        self.turns = torch.tensor(turns, dtype=torch.float64, device=device if device is not None else "cuda")
+
+
+def _heads(t, name, T, d, dtype):
+    """[T, heads, head_dim] with dense heads; returns (heads, token stride)."""
+    if t.dtype != dtype or t.dim() != 3 or t.shape[0] != T or t.shape[2] != d:
+        raise ValueError(f"{name} must be a {dtype} tensor [{T}, heads, {d}]")
+    h = t.shape[1]
+    if t.numel() and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d)):
+        raise ValueError(f"the heads of a token of {name} must be dense")
+    return h, (t.stride(0) if T > 1 else h * d)
+
+
+def _index(t, name, shape):
+    _dense(t, name, shape, (torch.int32,))
+
+
+def qlora_rope(q, k, table, positions, inverse=False, q_out=None, k_out=None, stream=None):
+    """Rotates q [T, heads, head_dim] and k (either may be None) to `positions`
+    (int32 [T]); tokens may be strided, float32 or bfloat16.  With `inverse`
+    the gradient of that.  Returns (q_out, k_out); q_out and k_out may be q and
+    k themselves."""
+    t = q if q is not None else k
+    if t is None or t.dim() != 3:
+        raise ValueError("q or k must be given, as [T, heads, head_dim]")
+    if t.dtype not in _DTYPES:
+        raise ValueError("q and k must be float32 or bfloat16")
+    T, d, dt = t.shape[0], t.shape[2], t.dtype
+    _index(positions, "positions", (T,))
+    qh = qs = qos = kh = ks = kos = 0
+    with _On(stream, q, k, table.turns, positions, q_out, k_out) as on:
+        if q is not None:
+            qh, qs = _heads(q, "q", T, d, dt)
+            q_out = torch.empty(q.shape, dtype=dt, device=q.device) if q_out is None else q_out
+            h, qos = _heads(q_out, "q_out", T, d, dt)
+            if h != qh:
+                raise ValueError("q_out must have the heads of q")
+        if k is not None:
+            kh, ks = _heads(k, "k", T, d, dt)
+            k_out = torch.empty(k.shape, dtype=dt, device=k.device) if k_out is None else k_out
+            h, kos = _heads(k_out, "k_out", T, d, dt)
+            if h != kh:
+                raise ValueError("k_out must have the heads of k")
+        _call("qlora_rope", _ptr(q), qs, qh, _ptr(q_out) if qh else None, qos, _ptr(k), ks, kh,
+              _ptr(k_out) if kh else None, kos, T, d, table.rot_dim, _DTYPES[dt], positions.data_ptr(),
+              table.turns.data_ptr(), table.mscale, int(table.interleaved), int(bool(inverse)), on.stream)
+    return (q_out if q is not None else None), (k_out if k is not None else None)
+
+
+# ------------------------------------------------------ paged key-value cache
+
+def _cache(k_cache, v_cache):
+    if k_cache.dim() != 4:
+        raise ValueError("the caches must be [num_pages, kv_heads, page_size, head_dim]")
+    _dense(k_cache, "k_cache", k_cache.shape, (torch.bfloat16,))
+    _dense(v_cache, "v_cache", k_cache.shape, (torch.bfloat16,))
+    return k_cache.shape
+
+
+def qlora_rope_cache_write(q, k, v, table, positions, slots, k_cache, v_cache, q_out=None, stream=None):
+    """Tokens entering the cache: returns the rotated q (None for q None) and
+    stores the rotated k and v [T, kv_heads, head_dim] in their slots (int32
+    [T]; a slot outside the cache is not stored) of the bfloat16 caches
+    [num_pages, kv_heads, page_size, head_dim].  `table` None: no rotation."""
+    pages, kvh, page, d = _cache(k_cache, v_cache)
+    T = k.shape[0]
+    bf = torch.bfloat16
+    _index(slots, "slots", (T,))
+    if table is not None:
+        _index(positions, "positions", (T,))
+    qh = qs = qos = 0
+    with _On(stream, k, v, q, table.turns if table is not None else None, positions, slots, k_cache, v_cache,
+             q_out) as on:
+        kh, ks = _heads(k, "k", T, d, bf)
+        vh, vs = _heads(v, "v", T, d, bf)
+        if kh != kvh or vh != kvh:
+            raise ValueError("k and v must have the cache's heads")
+        if q is not None:
+            qh, qs = _heads(q, "q", T, d, bf)
+            q_out = torch.empty(q.shape, dtype=bf, device=q.device) if q_out is None else q_out
+            h, qos = _heads(q_out, "q_out", T, d, bf)
+            if h != qh:
+                raise ValueError("q_out must have the heads of q")
+        rot, mscale, inter = (table.rot_dim, table.mscale, int(table.interleaved)) if table is not None else (0, 1.0, 0)
+        _call("qlora_rope_cache_write", _ptr(q), qs, qh, _ptr(q_out) if qh else None, qos, k.data_ptr(), ks,
+              v.data_ptr(), vs, kvh, T, d, rot, _ptr(positions) if rot else None,
+              table.turns.data_ptr() if rot else None, mscale, inter, slots.data_ptr(), k_cache.data_ptr(),
+              v_cache.data_ptr(), pages, page, on.stream)
+    return q_out if q is not None else None
+
+
+PagedPlan = collections.namedtuple("PagedPlan", "total_lens starts slots positions pages_needed")
+
+
+def qlora_paged_plan(cached_lens, new_lens, free_pages, block_table, page_size, tokens, out=None, stream=None):
+    """Pages, slots and positions of a batch (all int32): sequence s has
+    cached_lens[s] tokens in the cache and gets new_lens[s] more.  Takes pages
+    from the front of free_pages, writes them into block_table [S, columns],
+    and returns PagedPlan: total_lens [S], starts [S + 1], slots and positions
+    [tokens] (rows behind the last new token: -1 and 0) and pages_needed [1].
+    `out`: a PagedPlan of these shapes to write to."""
+    S = cached_lens.shape[0]
+    _index(cached_lens, "cached_lens", (S,))
+    _index(new_lens, "new_lens", (S,))
+    _index(free_pages, "free_pages", (free_pages.numel(),))
+    _index(block_table, "block_table", (S, block_table.shape[1]))
+    with _On(stream, cached_lens, new_lens, free_pages, block_table, *(out or ())) as on:
+        if out is None:
+            new = lambda n: torch.empty(n, dtype=torch.int32, device=cached_lens.device)  # noqa: E731
+            out = PagedPlan(new(S), new(S + 1), new(tokens), new(tokens), new(1))
+        else:
+            for name, n in zip(PagedPlan._fields, (S, S + 1, tokens, tokens, 1)):
+                _index(getattr(out, name), name, (n,))
+        _call("qlora_paged_plan", cached_lens.data_ptr(), new_lens.data_ptr(), S, page_size, free_pages.data_ptr(),
+              free_pages.numel(), block_table.data_ptr(), block_table.shape[1], tokens, out.total_lens.data_ptr(),
+              out.starts.data_ptr(), out.slots.data_ptr(), out.positions.data_ptr(), out.pages_needed.data_ptr(),
+              on.stream)
+    return out
+
+
+def qlora_paged_attention(q, k_cache, v_cache, block_table, lengths, scale=None, out=None, lse=None, stream=None):
+    """Attention of one new token per sequence over the cache: q bfloat16 [S,
+    heads, head_dim], block_table int32 [S, columns], lengths int32 [S] (tokens
+    in the cache, the new one among them), scale 1 / sqrt(head_dim) unless
+    given.  Returns bfloat16 [S, heads, head_dim] (zeros for a length of 0);
+    `lse` (float32 [S, heads]) receives the log of the sum of exponentials."""
+    pages, kvh, page, d = _cache(k_cache, v_cache)
+    S = q.shape[0]
+    H, qs = _heads(q, "q", S, d, torch.bfloat16)
+    _index(lengths, "lengths", (S,))
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [sequences, columns]")
+    cols = block_table.shape[1]
+    _index(block_table, "block_table", (S, cols))
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _On(stream, q, k_cache, v_cache, block_table, lengths, out, lse) as on:
+        if out is None:
+            out = torch.empty((S, H, d), dtype=torch.bfloat16, device=q.device)
+        else:
+            _dense(out, "out", (S, H, d), (torch.bfloat16,))
+        if lse is not None:
+            _dense(lse, "lse", (S, H), (torch.float32,))
+        nws = _i64(0)
+        _call("qlora_paged_attention_workspace", S, H, kvh, d, cols, page, ctypes.byref(nws))
+        ws = torch.empty(nws.value, dtype=torch.uint8, device=q.device) if nws.value else None
+        _call("qlora_paged_attention", q.data_ptr(), qs, S, H, kvh, d, k_cache.data_ptr(), v_cache.data_ptr(), pages,
+              page, block_table.data_ptr(), cols, lengths.data_ptr(), scale, out.data_ptr(), _ptr(lse), _ptr(ws),
+              nws.value, on.stream)
+    return out

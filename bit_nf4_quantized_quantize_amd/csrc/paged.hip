@@ -119,66 +119,286 @@ hipError_t launch_paged_plan(const PlanArgs& a, hipStream_t stream) {
 
 // -------------------------------------------------------------- attention
 //
-// One wave per sequence and query head: scores of 64 tokens at a time, a
-// token per lane; then the weighted sum of their values, four elements of the
-// head per lane.
+// Bound by HBM: every key and value of a sequence is read once, by the
+// workgroup that takes its kv head (and its share of the length).  The work
+// per byte is small but grows with the query heads that share a kv head, so
+// the products run on MFMA with those heads as the 16 columns; a wave works
+// alone on tiles of 32 tokens, with the running maximum and sum of its own:
+//   scores^T [32 tokens x 16 heads] = K Q^T, K straight from memory as the
+//     row operand (a lane holds 8 elements of a token's row), Q kept in
+//     registers;
+//   out^T [d x 16 heads] += V^T P, where the reduction index runs over the
+//     tokens in the order in which the scores' lanes hold them, so P goes from
+//     the exponentials into the operand without leaving its lane; V^T comes
+//     from a [token][d] tile in LDS by transposed reads.
+// The sums of the weights are fp32 sums of the weights before they are rounded
+// to bfloat16 for the product.  The rows of V behind the length are put as
+// zeros into LDS (0 times what lies there would not be 0 for an infinity), the
+// scores there are replaced, not added to.
 
 namespace {
 
-__global__ __launch_bounds__(64) void paged_attention_kernel(AttnArgs a) {
-  __shared__ float p_s[64];
-  __shared__ int64_t row_s[64];
+constexpr int kTile = 32;      // tokens per wave and step
+constexpr int kAttnWaves = 4;
+
+// How a sequence of n tokens is cut: `parts` ranges of `per` tiles (the last
+// may be shorter).  No range is shorter than one tile per wave.
+struct Cut {
+  int64_t tiles, per, parts;
+};
+__device__ __forceinline__ Cut cut_of(int64_t n, int splits) {
+  Cut c;
+  c.tiles = (n + kTile - 1) / kTile;
+  int64_t most = (c.tiles + kAttnWaves - 1) / kAttnWaves;
+  if (most > splits) most = splits;
+  if (most < 1) most = 1;
+  c.per = (c.tiles + most - 1) / most;
+  c.parts = c.per ? (c.tiles + c.per - 1) / c.per : 0;
+  return c;
+}
+
+__device__ __forceinline__ int64_t tokens_of(const AttnArgs& a, int64_t s) {
+  const int64_t n = a.lengths[s], cap = a.table_cols << a.page_shift;
+  return n < 0 ? 0 : n > cap ? cap : n;
+}
+
+// What the lanes of a wave hold of one tile.
+template <int DP>
+struct Tile {
+  uint4 k[2][DP / 32];  // tokens 16 half + lane % 16, elements 32 i + 8 (lane / 16) ..
+  uint4 v[DP / 16];     // pieces i * 64 + lane of the 32 rows
+  bool ok[2];           // the halves lie in pages of the cache
+};
+
+template <int DP>
+__device__ __forceinline__ void load_tile(Tile<DP>& t, const AttnArgs& a, const int32_t* table, int64_t tok, int64_t n,
+                                          int kv, int lane) {
+  constexpr int CH = DP / 8;  // 16-byte pieces of a padded row
+  const int d = a.head_dim;
+  int64_t base[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t first = tok + 16 * h;
+    int32_t page = -1;
+    if (first < n) page = table[first >> a.page_shift];
+    page = __builtin_amdgcn_readfirstlane(page);
+    t.ok[h] = page >= 0 && page < a.num_pages;
+    // without a page the loads go to the cache's first rows and count nothing
+    base[h] = t.ok[h] ? ((((int64_t)page * a.kv_heads + kv) << a.page_shift) + (first & ((1 << a.page_shift) - 1))) * d
+                      : 0;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint16_t* row = a.k_cache + base[h] + (lane & 15) * d;
+#pragma unroll
+    for (int i = 0; i < DP / 32; ++i) {
+      const int c = 32 * i + 8 * (lane >> 4);
+      t.k[h][i] = *reinterpret_cast<const uint4*>(row + (c < d ? c : 0));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < DP / 16; ++i) {
+    const int idx = i * 64 + lane, r = idx / CH, c = idx % CH * 8;
+    t.v[i] = *reinterpret_cast<const uint4*>(a.v_cache + (r < 16 ? base[0] : base[1]) + (r & 15) * d + (c < d ? c : 0));
+  }
+}
+
+template <int DP>
+__global__ __launch_bounds__(64 * kAttnWaves) void paged_attention_kernel(AttnArgs a, int qtiles) {
+  constexpr int CH = DP / 8;
+  constexpr int PITCH = DP + 16;  // of the V tile: 16 rows of one column go to different banks
+  constexpr int OP = DP + 4;      // of the partial outputs
+  constexpr int WAVE_BYTES = kTile * PITCH * 2;
+  static_assert(16 * OP * 4 <= WAVE_BYTES, "a wave's outputs take the place of its V tile");
+  __shared__ __attribute__((aligned(16))) char lds[kAttnWaves * WAVE_BYTES];
+  __shared__ float s_m[kAttnWaves][16], s_l[kAttnWaves][16];
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, col = lane & 15, d = a.head_dim;
   const int64_t s = blockIdx.y;
-  const int h = blockIdx.x, lane = threadIdx.x, d = a.head_dim;
-  const int j = h / (a.q_heads / a.kv_heads);
-  const int page = 1 << a.page_shift;
-  int64_t n = a.lengths[s];
-  const int64_t cap = a.table_cols << a.page_shift;
-  n = n < 0 ? 0 : n > cap ? cap : n;
-  const uint16_t* q = a.q + s * a.q_stride + (int64_t)h * d;
-  float m = -INFINITY, l = 0.0f, acc[4] = {0, 0, 0, 0};
-  for (int64_t t0 = 0; t0 < n; t0 += 64) {
-    const int64_t t = t0 + lane;
-    int64_t row = -1;
-    float sc = -INFINITY;
-    if (t < n) {
-      const int32_t pg = a.table[s * a.table_cols + (t >> a.page_shift)];
-      if (pg >= 0 && pg < a.num_pages) {
-        row = ((((int64_t)pg * a.kv_heads + j) << a.page_shift) + (t & (page - 1))) * d;
-        float dot = 0.0f;
-        for (int e = 0; e < d; ++e) dot = __builtin_fmaf(bf2f(q[e]), bf2f(a.k_cache[row + e]), dot);
-        sc = dot * a.scale;
+  int id = blockIdx.x;
+  const int z = id % a.splits;
+  id /= a.splits;
+  const int qt = id % qtiles, kv = id / qtiles;
+  const int group = a.q_heads / a.kv_heads;
+  const int h0 = kv * group + qt * 16, heads = group - qt * 16 < 16 ? group - qt * 16 : 16;
+  const int64_t n = tokens_of(a, s);
+  const Cut cut = cut_of(n, a.splits);
+  if (a.splits > 1 && z >= cut.parts) return;
+  const int64_t first = z * cut.per;
+  const int64_t last = first + cut.per < cut.tiles ? first + cut.per : cut.tiles;
+
+  // Q^T: column col (a query head), reduction elements 32 i + 8 g ..
+  bf16x8 q[DP / 32];
+#pragma unroll
+  for (int i = 0; i < DP / 32; ++i) {
+    const int c = 32 * i + 8 * g;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (col < heads && c < d)
+      v = *reinterpret_cast<const uint4*>(a.q + s * a.q_stride + (int64_t)(h0 + col) * d + c);
+    q[i] = __builtin_bit_cast(bf16x8, v);
+  }
+  const int32_t* table = a.table + s * a.table_cols;
+  const float scale2 = a.scale * 1.44269504088896340736f;  // scores in base 2
+  float m = -INFINITY, l = 0.0f;
+  floatx4 acc[DP / 16];
+#pragma unroll
+  for (int t = 0; t < DP / 16; ++t) acc[t] = (floatx4){0, 0, 0, 0};
+  __bf16* vt = reinterpret_cast<__bf16*>(lds + wave * WAVE_BYTES);
+
+  Tile<DP> t;
+  int64_t ti = first + wave;
+  if (ti < last) load_tile<DP>(t, a, table, ti * kTile, n, kv, lane);
+  for (; ti < last; ti += kAttnWaves) {
+    const int64_t tok = ti * kTile;
+    const bool full = tok + kTile <= n && t.ok[0] && t.ok[1];
+    // V to LDS
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i) {
+      const int idx = i * 64 + lane, r = idx / CH, c = idx % CH * 8;
+      uint4 v = t.v[i];
+      if (!full && !(tok + r < n && (r < 16 ? t.ok[0] : t.ok[1]))) v = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(vt + r * PITCH + c) = v;
+    }
+    // scores
+    floatx4 sc[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      sc[h] = (floatx4){0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < DP / 32; ++i) {
+        uint4 k = t.k[h][i];
+        if (d < DP && 32 * i + 8 * g >= d) k = make_uint4(0, 0, 0, 0);
+        sc[h] = mfma16(__builtin_bit_cast(bf16x8, k), q[i], sc[h]);
       }
     }
-    const float mt = fmaxf(m, wave_max(sc));
-    const float mu = mt == -INFINITY ? 0.0f : mt;
-    const float p = row < 0 ? 0.0f : expf(sc - mu), old = expf(m - mu);
-    m = mt;
-    float ps = p;
-    for (int o = 1; o < 64; o <<= 1) ps += __shfl_xor(ps, o, 64);
-    l = l * old + ps;
-    p_s[lane] = p;
-    row_s[lane] = row;
-    __syncthreads();
-    for (int i = 0; i < 4; ++i) acc[i] *= old;
-    for (int i = 0; i < 64; ++i) {
-      if (row_s[i] < 0) continue;
-      for (int e = 0; e < 4; ++e)
-        if (lane * 4 + e < d) acc[e] = __builtin_fmaf(p_s[i], bf2f(a.v_cache[row_s[i] + lane * 4 + e]), acc[e]);
+    const bool ok0 = t.ok[0], ok1 = t.ok[1];
+    if (ti + kAttnWaves < last) load_tile<DP>(t, a, table, tok + kAttnWaves * kTile, n, kv, lane);
+    float p[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = sc[j >> 2][j & 3] * scale2;
+    if (!full) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (!(tok + 16 * (j >> 2) + 4 * g + (j & 3) < n && (j < 4 ? ok0 : ok1))) p[j] = -INFINITY;
     }
-    __syncthreads();
+    float mt = m;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mt = fmaxf(mt, p[j]);
+    mt = fmaxf(mt, __shfl_xor(mt, 16, 64));
+    mt = fmaxf(mt, __shfl_xor(mt, 32, 64));
+    const float mu = mt == -INFINITY ? 0.0f : mt;
+    if (__ballot(mt > m)) {
+      const float old = __builtin_amdgcn_exp2f(m - mu);
+      l *= old;
+#pragma unroll
+      for (int i = 0; i < DP / 16; ++i) acc[i] *= old;
+    }
+    m = mt;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      p[j] = __builtin_amdgcn_exp2f(p[j] - mu);
+      l += p[j];
+    }
+    const uint4 pw = make_uint4(pack_bf2(p[0], p[1]), pack_bf2(p[2], p[3]), pack_bf2(p[4], p[5]), pack_bf2(p[6], p[7]));
+    const bf16x8 pb = __builtin_bit_cast(bf16x8, pw);
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i) {
+      const __bf16* src = vt + (4 * g + (col >> 2)) * PITCH + 16 * i + 4 * (col & 3);
+      const short4_t lo = ds_read_tr16(src), hi = ds_read_tr16(src + 16 * PITCH);
+      const short8_t v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      acc[i] = mfma16(__builtin_bit_cast(bf16x8, v), pb, acc[i]);
+    }
   }
-  for (int e = 0; e < 4; ++e)
-    if (lane * 4 + e < d) a.out[(s * a.q_heads + h) * d + lane * 4 + e] = f2bf(l > 0.0f ? acc[e] / l : 0.0f);
-  if (a.lse && lane == 0) a.lse[s * a.q_heads + h] = l > 0.0f ? m + logf(l) : -INFINITY;
+
+  // join the waves: each lane group holds the sum of its own tokens
+  l += __shfl_xor(l, 16, 64);
+  l += __shfl_xor(l, 32, 64);
+  if (g == 0) s_m[wave][col] = m, s_l[wave][col] = l;
+  __builtin_amdgcn_wave_barrier();
+  float* ow = reinterpret_cast<float*>(lds + wave * WAVE_BYTES);
+#pragma unroll
+  for (int i = 0; i < DP / 16; ++i) *reinterpret_cast<floatx4*>(ow + col * OP + 16 * i + 4 * g) = acc[i];
+  __syncthreads();
+  for (int e = threadIdx.x; e < heads * (d / 4); e += 64 * kAttnWaves) {
+    const int h = e / (d / 4), c = e % (d / 4) * 4;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) mx = fmaxf(mx, s_m[w][h]);
+    const float mu = mx == -INFINITY ? 0.0f : mx;
+    float sum = 0.0f;
+    floatx4 o = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) {
+      const float f = __builtin_amdgcn_exp2f(s_m[w][h] - mu);
+      sum += s_l[w][h] * f;
+      o += *reinterpret_cast<const floatx4*>(reinterpret_cast<const float*>(lds + w * WAVE_BYTES) + h * OP + c) * f;
+    }
+    const int64_t row = s * a.q_heads + h0 + h;
+    if (a.splits > 1) {
+      *reinterpret_cast<floatx4*>(a.part_o + (row * a.splits + z) * d + c) = o;
+      if (c == 0) a.part_ml[(row * a.splits + z) * 2] = mx, a.part_ml[(row * a.splits + z) * 2 + 1] = sum;
+    } else {
+      o *= sum == 0.0f ? 0.0f : 1.0f / sum;
+      *reinterpret_cast<uint2*>(a.out + row * d + c) = make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
+      if (a.lse && c == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994530942f;
+    }
+  }
+}
+
+// Joins the parts of a sequence, one wave per sequence and head, in order.
+__global__ __launch_bounds__(64) void paged_join_kernel(AttnArgs a) {
+  const int64_t s = blockIdx.y, row = s * a.q_heads + blockIdx.x;
+  const int lane = threadIdx.x, d = a.head_dim;
+  const int parts = (int)cut_of(tokens_of(a, s), a.splits).parts;
+  const float* ml = a.part_ml + row * a.splits * 2;
+  float mx = -INFINITY;
+  for (int z = 0; z < parts; ++z) mx = fmaxf(mx, ml[2 * z]);
+  const float mu = mx == -INFINITY ? 0.0f : mx;
+  float sum = 0.0f;
+  floatx4 o = {0, 0, 0, 0};
+  const bool mine = 4 * lane < d;
+  const float* src = a.part_o + row * a.splits * d + (mine ? 4 * lane : 0);
+  for (int z = 0; z < parts; ++z) {
+    const float f = __builtin_amdgcn_exp2f(ml[2 * z] - mu);
+    sum += ml[2 * z + 1] * f;
+    o += *reinterpret_cast<const floatx4*>(src + (int64_t)z * d) * f;
+  }
+  o *= sum == 0.0f ? 0.0f : 1.0f / sum;
+  if (mine)
+    *reinterpret_cast<uint2*>(a.out + row * d + 4 * lane) = make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
+  if (a.lse && lane == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994530942f;
+}
+
+template <int DP>
+void attention_as(const AttnArgs& a, hipStream_t stream) {
+  const int qtiles = (a.q_heads / a.kv_heads + 15) / 16;
+  hipLaunchKernelGGL(paged_attention_kernel<DP>, dim3((unsigned)(a.kv_heads * qtiles * a.splits), (unsigned)a.S),
+                     dim3(64 * kAttnWaves), 0, stream, a, qtiles);
 }
 
 }  // namespace
 
-int paged_splits(int64_t, int, int, int64_t) { return 1; }
+// Enough workgroups for 8 per CU, as far as the length gives each wave a tile.
+int paged_splits(int64_t S, int q_heads, int kv_heads, int64_t max_len) {
+  if (S == 0) return 1;
+  const int64_t wgs = S * kv_heads * ((q_heads / kv_heads + 15) / 16);
+  int64_t n = (8 * 256 + wgs - 1) / wgs;
+  const int64_t most = (max_len + kAttnWaves * kTile - 1) / (kAttnWaves * kTile);
+  if (n > most) n = most;
+  if (n > 64) n = 64;
+  return n < 1 ? 1 : (int)n;
+}
 
 hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL(paged_attention_kernel, dim3(a.q_heads, (unsigned)a.S), dim3(64), 0, stream, a);
+  if (a.head_dim <= 64) attention_as<64>(a, stream);
+  else if (a.head_dim <= 96) attention_as<96>(a, stream);
+  else if (a.head_dim <= 128) attention_as<128>(a, stream);
+  else attention_as<256>(a, stream);
+  if (a.splits > 1)
+    hipLaunchKernelGGL(paged_join_kernel, dim3(a.q_heads, (unsigned)a.S), dim3(64), 0, stream, a);
   return hipGetLastError();
 }
 

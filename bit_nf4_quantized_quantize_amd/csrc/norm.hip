@@ -334,11 +334,10 @@ __global__ __launch_bounds__(wg_threads(TPR)) void norm_bwd_kernel(NormArgs a, i
 }
 
 // The three sums over tokens from the partial sums, in a fixed order: a
-// workgroup takes 64 columns, its wave w the partials w, w + 4, ...
-__global__ __launch_bounds__(256) void norm_sums_kernel(NormArgs a, int64_t parts) {
-  __shared__ float s[4][64];
-  float* const outs[3] = {a.dw_post, a.dgate, a.dw_pre};
-  float* out = outs[blockIdx.y];
+// workgroup takes 64 columns, its wave w the partials w, w + 16, ...
+__global__ __launch_bounds__(1024) void norm_sums_kernel(NormArgs a, int64_t parts) {
+  __shared__ float s[16][64];
+  float* out = blockIdx.y == 0 ? a.dw_post : blockIdx.y == 1 ? a.dgate : a.dw_pre;
   if (!out) return;
   const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
   const int64_t col = (int64_t)blockIdx.x * 64 + l;
@@ -346,11 +345,15 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(NormArgs a, int64_t part
   if (col < a.D) {
     const float* p = a.part + (int64_t)blockIdx.y * parts * a.D + col;
 #pragma unroll 8
-    for (int64_t i = w; i < parts; i += 4) acc += p[i * a.D];
+    for (int64_t i = w; i < parts; i += 16) acc += p[i * a.D];
   }
   s[w][l] = acc;
   __syncthreads();
-  if (w == 0 && col < a.D) out[col] = (s[0][l] + s[1][l]) + (s[2][l] + s[3][l]);
+  if (w == 0 && col < a.D) {
+#pragma unroll
+    for (int k = 1; k < 16; ++k) acc += s[k][l];
+    out[col] = acc;
+  }
 }
 
 __global__ __launch_bounds__(256) void norm_zero_sums_kernel(NormArgs a) {
@@ -394,7 +397,7 @@ hipError_t bwd_as(const NormArgs& a, hipStream_t stream) {
   else
     hipLaunchKernelGGL((norm_bwd_kernel<XT, HT, TPR, NV, false, false>), dim3(grid), wg, 0, stream, a, parts);
   if (sums)
-    hipLaunchKernelGGL(norm_sums_kernel, dim3((unsigned)((a.D + 63) / 64), 3), dim3(256), 0, stream, a, parts);
+    hipLaunchKernelGGL(norm_sums_kernel, dim3((unsigned)((a.D + 63) / 64), 3), dim3(1024), 0, stream, a, parts);
   return hipGetLastError();
 }
 

@@ -22,39 +22,51 @@ constexpr int kPlanThreads = 512;
 
 __device__ __forceinline__ int pages_of(int64_t tokens, int page) { return (int)((tokens + page - 1) / page); }
 
-__global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
+// The largest s < n with v[s] <= i (v[0] <= i).
+__device__ __forceinline__ int last_at_most(const int32_t* v, int n, int64_t i) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (v[mid] <= i) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a, int per) {
   extern __shared__ int32_t lds[];  // starts [S + 1], first page taken [S + 1]
   __shared__ int32_t wave[2][kPlanThreads / 64];
   int32_t* starts = lds;
   int32_t* first = lds + a.S + 1;
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  int32_t run_t = 0, run_p = 0;
-  for (int s0 = 0; s0 < a.S; s0 += kPlanThreads) {
-    const int s = s0 + threadIdx.x;
-    int32_t c = 0, n = 0;
-    if (s < a.S) {
-      c = a.cached[s] < 0 ? 0 : a.cached[s];
-      n = a.fresh[s] < 0 ? 0 : a.fresh[s];
-    }
+  // thread t sums sequences t * per .., then the threads' sums are scanned
+  const int s0 = threadIdx.x * per, s1 = s0 + per < a.S ? s0 + per : a.S;
+  int32_t nt = 0, np = 0;
+#pragma unroll 4
+  for (int s = s0; s < s1; ++s) {
+    const int32_t c = a.cached[s] < 0 ? 0 : a.cached[s], n = a.fresh[s] < 0 ? 0 : a.fresh[s];
     const int32_t p = pages_of((int64_t)c + n, a.page_size) - pages_of(c, a.page_size);
-    int32_t vt = n, vp = p;  // inclusive sums over the wave
+    starts[s] = n, first[s] = p;
+    nt += n, np += p;
+  }
+  int32_t vt = nt, vp = np;  // inclusive sums over the wave
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int32_t ut = __shfl_up(vt, o, 64), up = __shfl_up(vp, o, 64);
-      if (lane >= o) vt += ut, vp += up;
-    }
-    if (lane == 63) wave[0][wv] = vt, wave[1][wv] = vp;
-    __syncthreads();
-    int32_t bt = run_t, bp = run_p;
-    for (int w = 0; w < kPlanThreads / 64; ++w) {
-      if (w < wv) bt += wave[0][w], bp += wave[1][w];
-      run_t += wave[0][w], run_p += wave[1][w];
-    }
-    if (s < a.S) {
-      starts[s] = bt + vt - n;
-      first[s] = bp + vp - p;
-    }
-    __syncthreads();
+  for (int o = 1; o < 64; o <<= 1) {
+    const int32_t ut = __shfl_up(vt, o, 64), up = __shfl_up(vp, o, 64);
+    if (lane >= o) vt += ut, vp += up;
+  }
+  if (lane == 63) wave[0][wv] = vt, wave[1][wv] = vp;
+  __syncthreads();
+  int32_t run_t = 0, run_p = 0;
+  vt -= nt, vp -= np;
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 64; ++w) {
+    if (w < wv) vt += wave[0][w], vp += wave[1][w];
+    run_t += wave[0][w], run_p += wave[1][w];
+  }
+  for (int s = s0; s < s1; ++s) {
+    const int32_t n = starts[s], p = first[s];
+    starts[s] = vt, first[s] = vp;
+    vt += n, vp += p;
   }
   if (threadIdx.x == 0) starts[a.S] = run_t, first[a.S] = run_p;
   __syncthreads();
@@ -68,42 +80,39 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
   if (gid == 0) *a.pages_needed = run_p;
   // new table entries, in the order of the free list
   for (int64_t i = gid; i < run_p; i += gsz) {
-    int lo = 0, hi = a.S;  // the last sequence whose first page is at or before i
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (first[mid] <= i) lo = mid; else hi = mid;
-    }
-    const int64_t col = pages_of(a.cached[lo] < 0 ? 0 : a.cached[lo], a.page_size) + (i - first[lo]);
-    if (col < a.table_cols) a.table[lo * a.table_cols + col] = i < a.n_free ? a.free_pages[i] : -1;
+    const int q = last_at_most(first, a.S, i);
+    const int64_t col = pages_of(a.cached[q] < 0 ? 0 : a.cached[q], a.page_size) + (i - first[q]);
+    if (col < a.table_cols) a.table[q * a.table_cols + col] = i < a.n_free ? a.free_pages[i] : -1;
   }
-  for (int64_t t = gid; t < a.T; t += gsz) {
-    int32_t slot = -1;
-    int64_t pos = 0;
-    if (t < run_t) {
-      int lo = 0, hi = a.S;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (starts[mid] <= t) lo = mid; else hi = mid;
-      }
-      const int32_t c = a.cached[lo] < 0 ? 0 : a.cached[lo];
-      pos = c + (t - starts[lo]);
-      const int64_t col = pos / a.page_size, have = pages_of(c, a.page_size);
-      int32_t page = -1;
-      if (col < a.table_cols) {
-        if (col < have) {
-          page = a.table[lo * a.table_cols + col];
-        } else {
-          const int64_t i = first[lo] + col - have;
-          if (i < a.n_free) page = a.free_pages[i];
+  // rows: a thread takes four in a row, searches for the first one's sequence
+  // and walks on from there
+  for (int64_t t0 = 4 * gid; t0 < a.T; t0 += 4 * gsz) {
+    int q = t0 < run_t ? last_at_most(starts, a.S, t0) : 0;
+    for (int64_t t = t0; t < t0 + 4 && t < a.T; ++t) {
+      int32_t slot = -1;
+      int64_t pos = 0;
+      if (t < run_t) {
+        while (starts[q + 1] <= t) ++q;  // t < starts[S]
+        const int32_t c = a.cached[q] < 0 ? 0 : a.cached[q];
+        pos = c + (t - starts[q]);
+        const int64_t col = pos / a.page_size, have = pages_of(c, a.page_size);
+        int32_t page = -1;
+        if (col < a.table_cols) {
+          if (col < have) {
+            page = a.table[q * a.table_cols + col];
+          } else {
+            const int64_t i = first[q] + col - have;
+            if (i < a.n_free) page = a.free_pages[i];
+          }
+        }
+        if (page >= 0) {
+          const int64_t v = (int64_t)page * a.page_size + pos % a.page_size;
+          slot = v < ((int64_t)1 << 31) ? (int32_t)v : -1;
         }
       }
-      if (page >= 0) {
-        const int64_t v = (int64_t)page * a.page_size + pos % a.page_size;
-        slot = v < ((int64_t)1 << 31) ? (int32_t)v : -1;
-      }
+      a.slots[t] = slot;
+      a.positions[t] = (int32_t)pos;
     }
-    a.slots[t] = slot;
-    a.positions[t] = (int32_t)pos;
   }
 }
 
@@ -113,7 +122,7 @@ hipError_t launch_paged_plan(const PlanArgs& a, hipStream_t stream) {
   int64_t wgs = (a.T + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
   wgs = wgs < 1 ? 1 : wgs > 256 ? 256 : wgs;
   hipLaunchKernelGGL(paged_plan_kernel, dim3((unsigned)wgs), dim3(kPlanThreads),
-                     2 * (size_t)(a.S + 1) * sizeof(int32_t), stream, a);
+                     2 * (size_t)(a.S + 1) * sizeof(int32_t), stream, a, (a.S + kPlanThreads - 1) / kPlanThreads);
   return hipGetLastError();
 }
 
@@ -348,28 +357,49 @@ __global__ __launch_bounds__(64 * kAttnWaves) void paged_attention_kernel(AttnAr
   }
 }
 
-// Joins the parts of a sequence, one wave per sequence and head, in order.
-__global__ __launch_bounds__(64) void paged_join_kernel(AttnArgs a) {
+// Joins the parts of a sequence, one workgroup per sequence and head: its
+// threads hold four elements of the head each and take the parts in turns of
+// 1024 / head_dim, then the turns' sums are added in order.
+constexpr int kMaxSplits = 64;
+
+__global__ __launch_bounds__(256) void paged_join_kernel(AttnArgs a) {
+  __shared__ float s_f[kMaxSplits], s_sum;
+  __shared__ floatx4 s_o[256];
   const int64_t s = blockIdx.y, row = s * a.q_heads + blockIdx.x;
-  const int lane = threadIdx.x, d = a.head_dim;
+  const int d = a.head_dim, dq = d / 4, t = threadIdx.x;
   const int parts = (int)cut_of(tokens_of(a, s), a.splits).parts;
-  const float* ml = a.part_ml + row * a.splits * 2;
-  float mx = -INFINITY;
-  for (int z = 0; z < parts; ++z) mx = fmaxf(mx, ml[2 * z]);
-  const float mu = mx == -INFINITY ? 0.0f : mx;
-  float sum = 0.0f;
-  floatx4 o = {0, 0, 0, 0};
-  const bool mine = 4 * lane < d;
-  const float* src = a.part_o + row * a.splits * d + (mine ? 4 * lane : 0);
-  for (int z = 0; z < parts; ++z) {
-    const float f = __builtin_amdgcn_exp2f(ml[2 * z] - mu);
-    sum += ml[2 * z + 1] * f;
-    o += *reinterpret_cast<const floatx4*>(src + (int64_t)z * d) * f;
+  if (t < 64) {
+    float m = -INFINITY, l = 0.0f;
+    if (t < parts) {
+      const float2 v = *reinterpret_cast<const float2*>(a.part_ml + (row * a.splits + t) * 2);
+      m = v.x, l = v.y;
+    }
+    const float mx = wave_max(m), mu = mx == -INFINITY ? 0.0f : mx;
+    const float f = __builtin_amdgcn_exp2f(m - mu);
+    l *= f;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) l += __shfl_xor(l, o, 64);
+    s_f[t] = f;
+    if (t == 0) {
+      s_sum = l == 0.0f ? 0.0f : 1.0f / l;
+      if (a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994530942f;
+    }
   }
-  o *= sum == 0.0f ? 0.0f : 1.0f / sum;
-  if (mine)
-    *reinterpret_cast<uint2*>(a.out + row * d + 4 * lane) = make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
-  if (a.lse && lane == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994530942f;
+  __syncthreads();
+  const int turns = 256 / dq, turn = t / dq, c = t - turn * dq;
+  floatx4 o = {0, 0, 0, 0};
+  if (turn < turns) {
+    const float* src = a.part_o + row * a.splits * d + 4 * c;
+#pragma unroll 4
+    for (int z = turn; z < parts; z += turns) o += *reinterpret_cast<const floatx4*>(src + (int64_t)z * d) * s_f[z];
+  }
+  s_o[t] = o;
+  __syncthreads();
+  if (t < dq) {
+    for (int k = 1; k < turns; ++k) o += s_o[k * dq + t];
+    o *= s_sum;
+    *reinterpret_cast<uint2*>(a.out + row * d + 4 * t) = make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
+  }
 }
 
 template <int DP>
@@ -388,7 +418,7 @@ int paged_splits(int64_t S, int q_heads, int kv_heads, int64_t max_len) {
   int64_t n = (8 * 256 + wgs - 1) / wgs;
   const int64_t most = (max_len + kAttnWaves * kTile - 1) / (kAttnWaves * kTile);
   if (n > most) n = most;
-  if (n > 64) n = 64;
+  if (n > kMaxSplits) n = kMaxSplits;
   return n < 1 ? 1 : (int)n;
 }
 
@@ -398,7 +428,7 @@ hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t stream) {
   else if (a.head_dim <= 128) attention_as<128>(a, stream);
   else attention_as<256>(a, stream);
   if (a.splits > 1)
-    hipLaunchKernelGGL(paged_join_kernel, dim3(a.q_heads, (unsigned)a.S), dim3(64), 0, stream, a);
+    hipLaunchKernelGGL(paged_join_kernel, dim3(a.q_heads, (unsigned)a.S), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -64,99 +64,140 @@ __device__ __forceinline__ T* cache_row(void* cache, int32_t slot, int head, con
   return (T*)cache + (((page * a.kv_heads + head) << a.page_shift) + off) * (int64_t)a.head_dim;
 }
 
+// n / d for n < 2^31 by one multiplication (Granlund and Montgomery, "Division
+// by invariant integers using multiplication", PLDI 1994).
+struct Div {
+  uint32_t mul, d;
+  int shift;
+};
+Div div_by(uint32_t d) {
+  Div v = {0, d, 0};
+  while (((uint64_t)1 << v.shift) < d) ++v.shift;
+  v.mul = (uint32_t)(((((uint64_t)1 << v.shift) - d) << 32) / d + 1);
+  return v;
+}
+__device__ __forceinline__ int operator/(int n, const Div& v) {
+  return (int)((__umulhi((uint32_t)n, v.mul) + (uint32_t)n) >> v.shift);
+}
+
+// One piece of work: 16 bytes of one head (of each half of its pairs).
+template <typename T, int EV>
+struct Unit {
+  Piece<T, EV> x, y;
+  T* dst;        // NULL: nothing to do
+  int a, b;      // elements of the head that x and y are (b < 0: x alone)
+  int trig;      // index into the cosines, or -1: copied
+};
+
 // The heads of a token are cut into units: rotated units (a piece of each
 // half of the pairs, or a piece of whole pairs when interleaved), then pieces
-// of the rest of the head.  blockIdx.y takes a share of a token's units.
-template <typename T, int EV, bool INTER>
-__global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, int nt) {
+// of the rest of the head; the values' heads are pieces throughout.
+// blockIdx.y takes a share of a token group's units.  A thread loads UN units
+// before it stores the first.
+template <typename T, int EV, bool INTER, int UN>
+__global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, int nt, Div by_units, Div by_hu, Div by_vu,
+                                                        Div by_half) {
   extern __shared__ float trig[];  // [nt][half] cosines, then as many sines
   const int half = a.rot_dim / 2;
   const int64_t t0 = (int64_t)blockIdx.x * nt;
   const int n = (int)(a.T - t0 < nt ? a.T - t0 : nt);
   float* cs = trig;
   float* sn = trig + nt * half;
-  for (int i = threadIdx.x; i < n * half; i += kThreads)
-    angle(a.positions[t0 + i / half], a.turns[i % half], a.mscale, a.inverse, cs + i, sn + i);
+  for (int i = threadIdx.x; i < n * half; i += kThreads) {
+    const int tk = i / by_half;
+    angle(a.positions[t0 + tk], a.turns[i - tk * half], a.mscale, a.inverse, cs + i, sn + i);
+  }
   __syncthreads();
 
   constexpr int PE = INTER ? (EV > 1 ? EV / 2 : 1) : EV;  // pairs per rotated unit
-  const int ru = half / PE, tu = (a.head_dim - a.rot_dim) / EV, hu = ru + tu;
-  const int vu = a.v ? a.head_dim / EV : 0;
-  const int qk = (a.q_heads + a.kv_heads) * hu;
-  const int units = qk + a.kv_heads * vu;
-  for (int i = blockIdx.y * kThreads + threadIdx.x; i < n * units; i += gridDim.y * kThreads) {
-    const int tk = i / units, u = i - tk * units;
-    const int64_t t = t0 + tk;
-    int32_t slot = 0;
-    if (a.slots) slot = a.slots[t];
-    const bool stored = slot >= 0 && slot < a.num_slots;
-    if (u >= qk) {  // values
-      const int head = (u - qk) / vu, e = (u - qk - head * vu) * EV;
-      if (stored)
-        st<T, EV>(cache_row<T>(a.v_cache, slot, head, a) + e,
-                  ld<T, EV>((const T*)a.v + t * a.v_stride + (int64_t)head * a.head_dim + e));
-      continue;
-    }
-    int head = u / hu;
-    const int w = u - head * hu;
-    const T* src;
-    T* dst;
-    if (head < a.q_heads) {
-      src = (const T*)a.q + t * a.q_stride + (int64_t)head * a.head_dim;
-      dst = (T*)a.qo + t * a.qo_stride + (int64_t)head * a.head_dim;
-    } else {
-      head -= a.q_heads;
-      src = (const T*)a.k + t * a.k_stride + (int64_t)head * a.head_dim;
-      if (a.slots) {
+  const int hu = by_hu.d, ru = half / PE, qk = (a.q_heads + a.kv_heads) * hu, units = by_units.d;
+  const int total = n * units, step = gridDim.y * kThreads;
+  for (int i0 = blockIdx.y * kThreads + threadIdx.x; i0 < total; i0 += UN * step) {
+    Unit<T, EV> w[UN];
+#pragma unroll
+    for (int j = 0; j < UN; ++j) {
+      const int i = i0 + j * step;
+      w[j].dst = nullptr;
+      if (i >= total) continue;
+      const int tk = i / by_units, u = i - tk * units;
+      const int64_t t = t0 + tk;
+      int32_t slot = 0;
+      if (a.slots) slot = a.slots[t];
+      const bool stored = slot >= 0 && slot < a.num_slots;
+      const T* src;
+      w[j].trig = w[j].b = -1;
+      if (u >= qk) {  // values
         if (!stored) continue;
-        dst = cache_row<T>(a.k_cache, slot, head, a);
+        const int head = (u - qk) / by_vu;
+        w[j].a = (u - qk - head * (int)by_vu.d) * EV;
+        src = (const T*)a.v + t * a.v_stride + (int64_t)head * a.head_dim;
+        w[j].dst = cache_row<T>(a.v_cache, slot, head, a);
       } else {
-        dst = (T*)a.ko + t * a.ko_stride + (int64_t)head * a.head_dim;
+        int head = u / by_hu;
+        const int r = u - head * hu;
+        if (head < a.q_heads) {
+          src = (const T*)a.q + t * a.q_stride + (int64_t)head * a.head_dim;
+          w[j].dst = (T*)a.qo + t * a.qo_stride + (int64_t)head * a.head_dim;
+        } else {
+          head -= a.q_heads;
+          if (a.slots && !stored) continue;
+          src = (const T*)a.k + t * a.k_stride + (int64_t)head * a.head_dim;
+          w[j].dst = a.slots ? cache_row<T>(a.k_cache, slot, head, a)
+                             : (T*)a.ko + t * a.ko_stride + (int64_t)head * a.head_dim;
+        }
+        if (r < ru) {
+          w[j].trig = tk * half + r * PE;
+          w[j].a = INTER ? 2 * r * PE : r * PE;
+          if (!INTER) w[j].b = half + r * PE;
+          else if (EV == 1) w[j].b = 2 * r + 1;
+        } else {
+          w[j].a = a.rot_dim + (r - ru) * EV;
+        }
       }
+      w[j].x = ld<T, EV>(src + w[j].a);
+      if (w[j].b >= 0) w[j].y = ld<T, EV>(src + w[j].b);
     }
-    if (w >= ru) {  // the part of the head without rotation
-      const int e = a.rot_dim + (w - ru) * EV;
-      st<T, EV>(dst + e, ld<T, EV>(src + e));
-      continue;
-    }
-    const float* c = cs + tk * half + w * PE;
-    const float* s = sn + tk * half + w * PE;
-    if (INTER && EV > 1) {
-      Piece<T, EV> v = ld<T, EV>(src + w * EV);
 #pragma unroll
-      for (int j = 0; j < EV / 2; ++j) {
-        const float x = to_f<T>(v.e[2 * j]), y = to_f<T>(v.e[2 * j + 1]);
-        v.e[2 * j] = from_f<T>(x * c[j] - y * s[j]);
-        v.e[2 * j + 1] = from_f<T>(x * s[j] + y * c[j]);
-      }
-      st<T, EV>(dst + w * EV, v);
-    } else {
-      const int ea = INTER ? 2 * w : w * EV, eb = INTER ? 2 * w + 1 : half + w * EV;
-      Piece<T, EV> x = ld<T, EV>(src + ea), y = ld<T, EV>(src + eb);
+    for (int j = 0; j < UN; ++j) {
+      if (!w[j].dst) continue;
+      if (w[j].trig >= 0) {
+        const float* c = cs + w[j].trig;
+        const float* s = sn + w[j].trig;
+        if (INTER && EV > 1) {
 #pragma unroll
-      for (int j = 0; j < EV; ++j) {
-        const float p = to_f<T>(x.e[j]), q = to_f<T>(y.e[j]);
-        x.e[j] = from_f<T>(p * c[j] - q * s[j]);
-        y.e[j] = from_f<T>(p * s[j] + q * c[j]);
+          for (int k = 0; k < EV / 2; ++k) {
+            const float x = to_f<T>(w[j].x.e[2 * k]), y = to_f<T>(w[j].x.e[2 * k + 1]);
+            w[j].x.e[2 * k] = from_f<T>(x * c[k] - y * s[k]);
+            w[j].x.e[2 * k + 1] = from_f<T>(x * s[k] + y * c[k]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < EV; ++k) {
+            const float x = to_f<T>(w[j].x.e[k]), y = to_f<T>(w[j].y.e[k]);
+            w[j].x.e[k] = from_f<T>(x * c[k] - y * s[k]);
+            w[j].y.e[k] = from_f<T>(x * s[k] + y * c[k]);
+          }
+        }
       }
-      st<T, EV>(dst + ea, x);
-      st<T, EV>(dst + eb, y);
+      st<T, EV>(w[j].dst + w[j].a, w[j].x);
+      if (w[j].b >= 0) st<T, EV>(w[j].dst + w[j].b, w[j].y);
     }
   }
 }
 
-template <typename T, int EV>
+template <typename T, int EV, bool INTER>
 hipError_t rope_as(const RopeArgs& a, hipStream_t stream) {
   // Few tokens: one token per workgroup and its units over several; many: four
   // tokens share a workgroup.
   const int nt = a.T >= 1024 ? 4 : 1;
   const int64_t gx = (a.T + nt - 1) / nt;
   const unsigned gy = gx >= 512 ? 1 : 4;
+  const int half = a.rot_dim / 2, pe = INTER ? (EV > 1 ? EV / 2 : 1) : EV;
+  const int hu = half / pe + (a.head_dim - a.rot_dim) / EV, vu = a.head_dim / EV;
+  const int units = (a.q_heads + a.kv_heads) * hu + (a.v ? a.kv_heads * vu : 0);
   const size_t lds = (size_t)nt * a.rot_dim * sizeof(float);
-  if (a.interleaved)
-    hipLaunchKernelGGL((rope_kernel<T, EV, true>), dim3((unsigned)gx, gy), dim3(kThreads), lds, stream, a, nt);
-  else
-    hipLaunchKernelGGL((rope_kernel<T, EV, false>), dim3((unsigned)gx, gy), dim3(kThreads), lds, stream, a, nt);
+  hipLaunchKernelGGL((rope_kernel<T, EV, INTER, 4>), dim3((unsigned)gx, gy), dim3(kThreads), lds, stream, a, nt,
+                     div_by(units), div_by(hu), div_by(vu), div_by(half ? half : 1));
   return hipGetLastError();
 }
 
@@ -169,8 +210,12 @@ hipError_t launch_rope(const RopeArgs& a, bool f32, hipStream_t stream) {
   const bool vec = a.head_dim % ev == 0 && (a.interleaved ? a.rot_dim : a.rot_dim / 2) % ev == 0 &&
                    a.rot_dim % ev == 0 && a.q_stride % ev == 0 && a.qo_stride % ev == 0 && a.k_stride % ev == 0 &&
                    a.ko_stride % ev == 0 && a.v_stride % ev == 0;
-  if (f32) return vec ? rope_as<float, 4>(a, stream) : rope_as<float, 1>(a, stream);
-  return vec ? rope_as<uint16_t, 8>(a, stream) : rope_as<uint16_t, 1>(a, stream);
+  if (a.interleaved) {
+    if (f32) return vec ? rope_as<float, 4, true>(a, stream) : rope_as<float, 1, true>(a, stream);
+    return vec ? rope_as<uint16_t, 8, true>(a, stream) : rope_as<uint16_t, 1, true>(a, stream);
+  }
+  if (f32) return vec ? rope_as<float, 4, false>(a, stream) : rope_as<float, 1, false>(a, stream);
+  return vec ? rope_as<uint16_t, 8, false>(a, stream) : rope_as<uint16_t, 1, false>(a, stream);
 }
 
 }  // namespace qlora

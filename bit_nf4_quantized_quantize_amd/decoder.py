@@ -11,7 +11,9 @@ there, so their memory is not handed out again before the call has run.
 """
 
 import collections
+import contextlib
 import ctypes
+import functools
 import math
 
 import torch
@@ -67,62 +69,62 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-class _On:
-    """Makes the device of `tensors` and `stream` (if given) current; .stream
-    is the handle to launch on."""
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
-    __slots__ = ("stream", "_guards")
 
-    def __init__(self, stream, *tensors):
-        dev = None
-        for t in tensors:
-            if t is None:
-                continue
-            if not t.is_cuda:
-                raise ValueError("qlora_nf4 tensors must live on a HIP device")
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError("all tensors of a call must be on one device")
-        self._guards = ()
-        if stream is None:
-            if dev.index != torch.cuda.current_device():
-                self._guards = (torch.cuda.device(dev),)
-            stream = torch.cuda.current_stream(dev)
-        elif stream != torch.cuda.current_stream(dev):
-            if stream.device != dev:
-                raise ValueError("stream must belong to the tensors' device")
-            self._guards = (torch.cuda.stream(stream),)
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
-        elif dev.index != torch.cuda.current_device():
-            self._guards = (torch.cuda.device(dev),)
-        self.stream = stream.cuda_stream
+def _here(stream, *tensors):
+    """The handle of the stream to launch on if the call can run as things
+    stand (the tensors' device is the current one and `stream`, if given, its
+    current stream), else None."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            i = t.get_device()
+            if i != dev:
+                if i < 0:
+                    raise ValueError("qlora_nf4 tensors must live on a HIP device")
+                if dev is not None:
+                    raise ValueError("all tensors of a call must be on one device")
+                dev = i
+    if dev != torch.cuda.current_device():
+        return None
+    raw = _raw_stream(dev)
+    return raw if stream is None or (stream.cuda_stream == raw and stream.device_index == dev) else None
 
-    def __enter__(self):
-        for g in self._guards:
-            g.__enter__()
-        return self
 
-    def __exit__(self, *e):
-        for g in self._guards:
-            g.__exit__(*e)
+@contextlib.contextmanager
+def _there(stream, *tensors):
+    """Makes the tensors' device, and `stream` if given, current, for a call that
+    cannot run as things stand."""
+    given = [t for t in tensors if t is not None]
+    dev = given[0].device
+    if stream is None:
+        with torch.cuda.device(dev):
+            yield
+        return
+    if stream.device != dev:
+        raise ValueError("stream must belong to the tensors' device")
+    for t in given:
+        t.record_stream(stream)
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        yield
 
 
 def _dense(t, name, shape, dtypes):
-    if t.dtype not in dtypes or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} and type "
                          f"{' or '.join(str(d) for d in dtypes)}")
 
 
-def _gain(t, name, D):
-    if t is not None:
-        _dense(t, name, (D,), (torch.float32,))
+def _gain(t, name, shape):
+    if t is not None and (t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape}")
 
 
 def _call(name, *args):
-    B._check(getattr(_lib or lib(), name)(*args), name)
+    status = getattr(_lib or lib(), name)(*args)
+    if status:
+        B._check(status, name)
 
 
 # --------------------------------------------------- norm, gate and residual
@@ -135,36 +137,46 @@ def qlora_norm_residual_fwd(x, h=None, w_pre=None, w_post=None, gate=None, alpha
     float32 [D] or None.  Returns (xo, n): xo is x when h is None, n is None
     without w_pre and has h's type (n_dtype, or x's, without h).  xo may be
     given as x itself: the stream is then updated in place."""
-    D = x.shape[-1]
-    T = x.numel() // D if D else 0
-    _dense(x, "x", x.shape, _DTYPES)
+    shape, xt = x.shape, x.dtype
+    D = shape[-1]
+    _dense(x, "x", shape, _DTYPES)
     if h is not None:
-        _dense(h, "h", x.shape, _DTYPES)
+        _dense(h, "h", shape, _DTYPES)
         nd = h.dtype
         if n_dtype is not None and n_dtype != nd:
             raise ValueError("n has the type of h")
     else:
-        nd = n_dtype if n_dtype is not None else x.dtype
+        nd = n_dtype if n_dtype is not None else xt
         if nd not in _DTYPES:
             raise ValueError("n_dtype must be torch.float32 or torch.bfloat16")
-    _gain(w_pre, "w_pre", D)
-    _gain(w_post, "w_post", D)
-    _gain(gate, "gate", D)
-    with _On(stream, x, h, w_pre, w_post, gate, xo, n) as on:
-        if xo is not None:
-            _dense(xo, "xo", x.shape, (x.dtype,))
-        elif h is not None:
-            xo = torch.empty_like(x)
-        if n is not None:
-            _dense(n, "n", x.shape, (nd,))
-        elif w_pre is not None:
-            n = torch.empty_like(x, dtype=nd)
-        _call("qlora_norm_residual_fwd", x.data_ptr(), _DTYPES[x.dtype], _ptr(h), _DTYPES[nd], T, D, _ptr(w_post),
-              _ptr(gate), alpha, _ptr(w_pre), eps, _ptr(xo), _ptr(n), on.stream)
+    _gain(w_pre, "w_pre", (D,))
+    _gain(w_post, "w_post", (D,))
+    _gain(gate, "gate", (D,))
+    on = _here(stream, x, h, w_pre, w_post, gate, xo, n)
+    if on is None:
+        with _there(stream, x, h, w_pre, w_post, gate, xo, n):
+            return qlora_norm_residual_fwd(x, h, w_pre, w_post, gate, alpha, eps, n_dtype, xo, n)
+    if xo is not None:
+        _dense(xo, "xo", shape, (xt,))
+    elif h is not None:
+        xo = torch.empty_like(x)
+    if n is not None:
+        _dense(n, "n", shape, (nd,))
+    elif w_pre is not None:
+        n = torch.empty_like(x, dtype=nd)
+    _call("qlora_norm_residual_fwd", x.data_ptr(), _DTYPES[xt], _ptr(h), _DTYPES[nd], x.numel() // D if D else 0, D,
+          _ptr(w_post), _ptr(gate), alpha, _ptr(w_pre), eps, _ptr(xo), _ptr(n), on)
     return (x if xo is None else xo), n
 
 
 NormGrads = collections.namedtuple("NormGrads", "dx dh dw_pre dw_post dgate")
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_bwd_workspace(T, D, xt, ht):
+    nws = _i64(0)
+    _call("qlora_norm_residual_bwd_workspace", T, D, xt, ht, 3, ctypes.byref(nws))
+    return nws.value
 
 
 def qlora_norm_residual_bwd(dxo, dn, xo, h=None, w_pre=None, w_post=None, gate=None, alpha=1.0, eps=1e-6,
@@ -174,31 +186,39 @@ def qlora_norm_residual_bwd(dxo, dn, xo, h=None, w_pre=None, w_post=None, gate=N
     for w_post and the gradient of the gate).  Returns NormGrads: dx, dh (None
     without need_dh) and, with need_gains, the float32 gradients of the gains
     and the gate that the forward had."""
-    D = xo.shape[-1]
+    shape, xt = xo.shape, xo.dtype
+    D = shape[-1]
     T = xo.numel() // D if D else 0
-    _dense(xo, "xo", xo.shape, _DTYPES)
-    hd = next((t.dtype for t in (h, dn, dh) if t is not None), xo.dtype)
-    for t, name, dt in ((dxo, "dxo", xo.dtype), (dx, "dx", xo.dtype), (dn, "dn", hd), (h, "h", hd), (dh, "dh", hd)):
+    _dense(xo, "xo", shape, _DTYPES)
+    hd = next((t.dtype for t in (h, dn, dh) if t is not None), xt)
+    if hd not in _DTYPES:
+        raise ValueError("h, dn and dh must be float32 or bfloat16")
+    for t, name, dt in ((dxo, "dxo", xt), (dx, "dx", xt), (dn, "dn", hd), (h, "h", hd), (dh, "dh", hd)):
         if t is not None:
-            _dense(t, name, xo.shape, (dt,) if dt in _DTYPES else _DTYPES)
-    _gain(w_pre, "w_pre", D)
-    _gain(w_post, "w_post", D)
-    _gain(gate, "gate", D)
-    with _On(stream, xo, dxo, dn, h, w_pre, w_post, gate, dx, dh) as on:
-        dx = torch.empty_like(xo) if dx is None else dx
-        if dh is None and need_dh:
-            dh = torch.empty_like(xo, dtype=hd)
+            _dense(t, name, shape, (dt,))
+    _gain(w_pre, "w_pre", (D,))
+    _gain(w_post, "w_post", (D,))
+    _gain(gate, "gate", (D,))
+    on = _here(stream, xo, dxo, dn, h, w_pre, w_post, gate, dx, dh)
+    if on is None:
+        with _there(stream, xo, dxo, dn, h, w_pre, w_post, gate, dx, dh):
+            return qlora_norm_residual_bwd(dxo, dn, xo, h, w_pre, w_post, gate, alpha, eps, need_dh, need_gains, dx,
+                                           dh)
+    dx = torch.empty_like(xo) if dx is None else dx
+    if dh is None and need_dh:
+        dh = torch.empty_like(xo, dtype=hd)
+    dw_pre = dw_post = dgate = ws = None
+    nws = 0
+    if need_gains:
         new = lambda: torch.empty(D, dtype=torch.float32, device=xo.device)  # noqa: E731
-        dw_pre = new() if need_gains and dn is not None else None
-        dw_post = new() if need_gains and w_post is not None else None
-        dgate = new() if need_gains and gate is not None else None
-        ws, nws = None, _i64(0)
-        if dw_pre is not None or dw_post is not None or dgate is not None:
-            _call("qlora_norm_residual_bwd_workspace", T, D, _DTYPES[xo.dtype], _DTYPES[hd], 3, ctypes.byref(nws))
-            ws = torch.empty(max(nws.value, 16), dtype=torch.uint8, device=xo.device)
-        _call("qlora_norm_residual_bwd", _ptr(dxo), xo.data_ptr(), _DTYPES[xo.dtype], _ptr(dn), _ptr(h), _DTYPES[hd],
-              T, D, _ptr(w_post), _ptr(gate), alpha, _ptr(w_pre), eps, dx.data_ptr(), _ptr(dh), _ptr(dw_post),
-              _ptr(dgate), _ptr(dw_pre), _ptr(ws), nws.value, on.stream)
+        dw_pre = new() if dn is not None else None
+        dw_post = new() if w_post is not None else None
+        dgate = new() if gate is not None else None
+        nws = _norm_bwd_workspace(T, D, _DTYPES[xt], _DTYPES[hd])
+        ws = torch.empty(nws, dtype=torch.uint8, device=xo.device)
+    _call("qlora_norm_residual_bwd", _ptr(dxo), xo.data_ptr(), _DTYPES[xt], _ptr(dn), _ptr(h), _DTYPES[hd], T, D,
+          _ptr(w_post), _ptr(gate), alpha, _ptr(w_pre), eps, dx.data_ptr(), _ptr(dh), _ptr(dw_post), _ptr(dgate),
+          _ptr(dw_pre), _ptr(ws), nws, on)
     return NormGrads(dx, dh, dw_pre, dw_post, dgate)
 
 
@@ -231,16 +251,21 @@ class RopeTable:
 
 def _heads(t, name, T, d, dtype):
     """[T, heads, head_dim] with dense heads; returns (heads, token stride)."""
-    if t.dtype != dtype or t.dim() != 3 or t.shape[0] != T or t.shape[2] != d:
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != d or t.dtype != dtype:
         raise ValueError(f"{name} must be a {dtype} tensor [{T}, heads, {d}]")
-    h = t.shape[1]
-    if t.numel() and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d)):
+    h = shape[1]
+    if t.is_contiguous():
+        return h, h * d
+    st = t.stride()
+    if (d > 1 and st[2] != 1) or (h > 1 and st[1] != d):
         raise ValueError(f"the heads of a token of {name} must be dense")
-    return h, (t.stride(0) if T > 1 else h * d)
+    return h, (st[0] if T > 1 else h * d)
 
 
 def _index(t, name, shape):
-    _dense(t, name, shape, (torch.int32,))
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}")
 
 
 def qlora_rope(q, k, table, positions, inverse=False, q_out=None, k_out=None, stream=None):
@@ -251,38 +276,50 @@ def qlora_rope(q, k, table, positions, inverse=False, q_out=None, k_out=None, st
     t = q if q is not None else k
     if t is None or t.dim() != 3:
         raise ValueError("q or k must be given, as [T, heads, head_dim]")
-    if t.dtype not in _DTYPES:
+    dt = t.dtype
+    if dt not in _DTYPES:
         raise ValueError("q and k must be float32 or bfloat16")
-    T, d, dt = t.shape[0], t.shape[2], t.dtype
+    T, _, d = t.shape
     _index(positions, "positions", (T,))
+    on = _here(stream, q, k, table.turns, positions, q_out, k_out)
+    if on is None:
+        with _there(stream, q, k, table.turns, positions, q_out, k_out):
+            return qlora_rope(q, k, table, positions, inverse, q_out, k_out)
     qh = qs = qos = kh = ks = kos = 0
-    with _On(stream, q, k, table.turns, positions, q_out, k_out) as on:
-        if q is not None:
-            qh, qs = _heads(q, "q", T, d, dt)
-            q_out = torch.empty(q.shape, dtype=dt, device=q.device) if q_out is None else q_out
-            h, qos = _heads(q_out, "q_out", T, d, dt)
-            if h != qh:
-                raise ValueError("q_out must have the heads of q")
-        if k is not None:
-            kh, ks = _heads(k, "k", T, d, dt)
-            k_out = torch.empty(k.shape, dtype=dt, device=k.device) if k_out is None else k_out
-            h, kos = _heads(k_out, "k_out", T, d, dt)
-            if h != kh:
-                raise ValueError("k_out must have the heads of k")
-        _call("qlora_rope", _ptr(q), qs, qh, _ptr(q_out) if qh else None, qos, _ptr(k), ks, kh,
-              _ptr(k_out) if kh else None, kos, T, d, table.rot_dim, _DTYPES[dt], positions.data_ptr(),
-              table.turns.data_ptr(), table.mscale, int(table.interleaved), int(bool(inverse)), on.stream)
-    return (q_out if q is not None else None), (k_out if k is not None else None)
+    if q is not None:
+        qh, qs = _heads(q, "q", T, d, dt)
+        q_out = torch.empty(q.shape, dtype=dt, device=q.device) if q_out is None else q_out
+        h, qos = _heads(q_out, "q_out", T, d, dt)
+        if h != qh:
+            raise ValueError("q_out must have the heads of q")
+    else:
+        q_out = None
+    if k is not None:
+        kh, ks = _heads(k, "k", T, d, dt)
+        k_out = torch.empty(k.shape, dtype=dt, device=k.device) if k_out is None else k_out
+        h, kos = _heads(k_out, "k_out", T, d, dt)
+        if h != kh:
+            raise ValueError("k_out must have the heads of k")
+    else:
+        k_out = None
+    _call("qlora_rope", _ptr(q), qs, qh, _ptr(q_out), qos, _ptr(k), ks, kh, _ptr(k_out), kos, T, d, table.rot_dim,
+          _DTYPES[dt], positions.data_ptr(), table.turns.data_ptr(), table.mscale, table.interleaved, bool(inverse),
+          on)
+    return q_out, k_out
 
 
 # ------------------------------------------------------ paged key-value cache
 
+_BF16 = (torch.bfloat16,)
+
+
 def _cache(k_cache, v_cache):
-    if k_cache.dim() != 4:
+    shape = k_cache.shape
+    if len(shape) != 4:
         raise ValueError("the caches must be [num_pages, kv_heads, page_size, head_dim]")
-    _dense(k_cache, "k_cache", k_cache.shape, (torch.bfloat16,))
-    _dense(v_cache, "v_cache", k_cache.shape, (torch.bfloat16,))
-    return k_cache.shape
+    _dense(k_cache, "k_cache", shape, _BF16)
+    _dense(v_cache, "v_cache", shape, _BF16)
+    return shape
 
 
 def qlora_rope_cache_write(q, k, v, table, positions, slots, k_cache, v_cache, q_out=None, stream=None):
@@ -294,27 +331,35 @@ def qlora_rope_cache_write(q, k, v, table, positions, slots, k_cache, v_cache, q
     T = k.shape[0]
     bf = torch.bfloat16
     _index(slots, "slots", (T,))
+    turns, rot, mscale, inter = None, 0, 1.0, False
     if table is not None:
+        turns, rot, mscale, inter = table.turns, table.rot_dim, table.mscale, table.interleaved
         _index(positions, "positions", (T,))
+    else:
+        positions = None
+    on = _here(stream, k, v, q, turns, positions, slots, k_cache, v_cache, q_out)
+    if on is None:
+        with _there(stream, k, v, q, turns, positions, slots, k_cache, v_cache, q_out):
+            return qlora_rope_cache_write(q, k, v, table, positions, slots, k_cache, v_cache, q_out)
+    kh, ks = _heads(k, "k", T, d, bf)
+    vh, vs = _heads(v, "v", T, d, bf)
+    if kh != kvh or vh != kvh:
+        raise ValueError("k and v must have the cache's heads")
     qh = qs = qos = 0
-    with _On(stream, k, v, q, table.turns if table is not None else None, positions, slots, k_cache, v_cache,
-             q_out) as on:
-        kh, ks = _heads(k, "k", T, d, bf)
-        vh, vs = _heads(v, "v", T, d, bf)
-        if kh != kvh or vh != kvh:
-            raise ValueError("k and v must have the cache's heads")
-        if q is not None:
-            qh, qs = _heads(q, "q", T, d, bf)
-            q_out = torch.empty(q.shape, dtype=bf, device=q.device) if q_out is None else q_out
+    if q is not None:
+        qh, qs = _heads(q, "q", T, d, bf)
+        if q_out is None:
+            q_out, qos = torch.empty(q.shape, dtype=bf, device=q.device), qh * d
+        else:
             h, qos = _heads(q_out, "q_out", T, d, bf)
             if h != qh:
                 raise ValueError("q_out must have the heads of q")
-        rot, mscale, inter = (table.rot_dim, table.mscale, int(table.interleaved)) if table is not None else (0, 1.0, 0)
-        _call("qlora_rope_cache_write", _ptr(q), qs, qh, _ptr(q_out) if qh else None, qos, k.data_ptr(), ks,
-              v.data_ptr(), vs, kvh, T, d, rot, _ptr(positions) if rot else None,
-              table.turns.data_ptr() if rot else None, mscale, inter, slots.data_ptr(), k_cache.data_ptr(),
-              v_cache.data_ptr(), pages, page, on.stream)
-    return q_out if q is not None else None
+    else:
+        q_out = None
+    _call("qlora_rope_cache_write", _ptr(q), qs, qh, _ptr(q_out), qos, k.data_ptr(), ks, v.data_ptr(), vs, kvh, T, d,
+          rot, _ptr(positions), _ptr(turns), mscale, inter, slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          pages, page, on)
+    return q_out
 
 
 PagedPlan = collections.namedtuple("PagedPlan", "total_lens starts slots positions pages_needed")
@@ -325,25 +370,38 @@ def qlora_paged_plan(cached_lens, new_lens, free_pages, block_table, page_size, 
     cached_lens[s] tokens in the cache and gets new_lens[s] more.  Takes pages
     from the front of free_pages, writes them into block_table [S, columns],
     and returns PagedPlan: total_lens [S], starts [S + 1], slots and positions
-    [tokens] (rows behind the last new token: -1 and 0) and pages_needed [1].
-    `out`: a PagedPlan of these shapes to write to."""
+    [tokens] (rows behind the last new token: -1 and 0) and pages_needed [1],
+    parts of one allocation.  `out`: a PagedPlan of these shapes to write to."""
     S = cached_lens.shape[0]
     _index(cached_lens, "cached_lens", (S,))
     _index(new_lens, "new_lens", (S,))
-    _index(free_pages, "free_pages", (free_pages.numel(),))
-    _index(block_table, "block_table", (S, block_table.shape[1]))
-    with _On(stream, cached_lens, new_lens, free_pages, block_table, *(out or ())) as on:
-        if out is None:
-            new = lambda n: torch.empty(n, dtype=torch.int32, device=cached_lens.device)  # noqa: E731
-            out = PagedPlan(new(S), new(S + 1), new(tokens), new(tokens), new(1))
-        else:
-            for name, n in zip(PagedPlan._fields, (S, S + 1, tokens, tokens, 1)):
-                _index(getattr(out, name), name, (n,))
-        _call("qlora_paged_plan", cached_lens.data_ptr(), new_lens.data_ptr(), S, page_size, free_pages.data_ptr(),
-              free_pages.numel(), block_table.data_ptr(), block_table.shape[1], tokens, out.total_lens.data_ptr(),
-              out.starts.data_ptr(), out.slots.data_ptr(), out.positions.data_ptr(), out.pages_needed.data_ptr(),
-              on.stream)
+    nfree = free_pages.numel()
+    _index(free_pages, "free_pages", (nfree,))
+    cols = block_table.shape[-1]
+    _index(block_table, "block_table", (S, cols))
+    on = _here(stream, cached_lens, new_lens, free_pages, block_table, *(out or ()))
+    if on is None:
+        with _there(stream, cached_lens, new_lens, free_pages, block_table, *(out or ())):
+            return qlora_paged_plan(cached_lens, new_lens, free_pages, block_table, page_size, tokens, out)
+    if out is None:
+        sizes = (S, S + 1, tokens, tokens, 1)
+        out = PagedPlan(*torch.empty(2 * (S + tokens + 1), dtype=torch.int32, device=cached_lens.device)
+                        .split_with_sizes(sizes))
+    else:
+        for name, n in zip(PagedPlan._fields, (S, S + 1, tokens, tokens, 1)):
+            _index(getattr(out, name), name, (n,))
+    total, starts, slots, positions, needed = out
+    _call("qlora_paged_plan", cached_lens.data_ptr(), new_lens.data_ptr(), S, page_size, free_pages.data_ptr(), nfree,
+          block_table.data_ptr(), cols, tokens, total.data_ptr(), starts.data_ptr(), slots.data_ptr(),
+          positions.data_ptr(), needed.data_ptr(), on)
     return out
+
+
+@functools.lru_cache(maxsize=256)
+def _attention_workspace(S, H, kvh, d, cols, page):
+    nws = _i64(0)
+    _call("qlora_paged_attention_workspace", S, H, kvh, d, cols, page, ctypes.byref(nws))
+    return nws.value
 
 
 def qlora_paged_attention(q, k_cache, v_cache, block_table, lengths, scale=None, out=None, lse=None, stream=None):
@@ -356,23 +414,22 @@ def qlora_paged_attention(q, k_cache, v_cache, block_table, lengths, scale=None,
     S = q.shape[0]
     H, qs = _heads(q, "q", S, d, torch.bfloat16)
     _index(lengths, "lengths", (S,))
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [sequences, columns]")
-    cols = block_table.shape[1]
+    cols = block_table.shape[-1]
     _index(block_table, "block_table", (S, cols))
+    on = _here(stream, q, k_cache, v_cache, block_table, lengths, out, lse)
+    if on is None:
+        with _there(stream, q, k_cache, v_cache, block_table, lengths, out, lse):
+            return qlora_paged_attention(q, k_cache, v_cache, block_table, lengths, scale, out, lse)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    with _On(stream, q, k_cache, v_cache, block_table, lengths, out, lse) as on:
-        if out is None:
-            out = torch.empty((S, H, d), dtype=torch.bfloat16, device=q.device)
-        else:
-            _dense(out, "out", (S, H, d), (torch.bfloat16,))
-        if lse is not None:
-            _dense(lse, "lse", (S, H), (torch.float32,))
-        nws = _i64(0)
-        _call("qlora_paged_attention_workspace", S, H, kvh, d, cols, page, ctypes.byref(nws))
-        ws = torch.empty(nws.value, dtype=torch.uint8, device=q.device) if nws.value else None
-        _call("qlora_paged_attention", q.data_ptr(), qs, S, H, kvh, d, k_cache.data_ptr(), v_cache.data_ptr(), pages,
-              page, block_table.data_ptr(), cols, lengths.data_ptr(), scale, out.data_ptr(), _ptr(lse), _ptr(ws),
-              nws.value, on.stream)
+    if out is None:
+        out = torch.empty((S, H, d), dtype=torch.bfloat16, device=q.device)
+    else:
+        _dense(out, "out", (S, H, d), _BF16)
+    if lse is not None:
+        _dense(lse, "lse", (S, H), (torch.float32,))
+    nws = _attention_workspace(S, H, kvh, d, cols, page)
+    ws = torch.empty(nws, dtype=torch.uint8, device=q.device) if nws else None
+    _call("qlora_paged_attention", q.data_ptr(), qs, S, H, kvh, d, k_cache.data_ptr(), v_cache.data_ptr(), pages, page,
+          block_table.data_ptr(), cols, lengths.data_ptr(), scale, out.data_ptr(), _ptr(lse), _ptr(ws), nws, on)
     return out

@@ -8,6 +8,24 @@
 
 namespace qlora {
 
+// n / d for n < 2^31 by one multiplication (Granlund and Montgomery, "Division
+// by invariant integers using multiplication", PLDI 1994).
+struct Div {
+  uint32_t mul, d;
+  int shift;
+};
+inline Div div_by(uint32_t d) {
+  Div v = {0, d, 0};
+  while (((uint64_t)1 << v.shift) < d) ++v.shift;
+  v.mul = (uint32_t)(((((uint64_t)1 << v.shift) - d) << 32) / d + 1);
+  return v;
+}
+#ifdef __HIPCC__
+__device__ __forceinline__ int operator/(int n, const Div& v) {
+  return (int)((__umulhi((uint32_t)n, v.mul) + (uint32_t)n) >> v.shift);
+}
+#endif
+
 // Residual update (include/qlora_decoder.h, qlora_norm_residual_*).
 struct NormArgs {
   const void* x;   // forward: the stream before; backward: xo, the stream after

@@ -20,7 +20,15 @@ namespace {
 
 constexpr int kPlanThreads = 512;
 
-__device__ __forceinline__ int pages_of(int64_t tokens, int page) { return (int)((tokens + page - 1) / page); }
+__device__ __forceinline__ int pages_of(int32_t tokens, const Div& page) {
+  return tokens > 0 ? (tokens - 1) / page + 1 : 0;
+}
+// A sequence's length from one of the caller's: not negative.
+__device__ __forceinline__ int32_t length_of(const int32_t* v, int64_t s) { return v[s] < 0 ? 0 : v[s]; }
+__device__ __forceinline__ int32_t clamped_sum(int32_t c, int32_t n) {
+  const int64_t v = (int64_t)c + n;
+  return v > INT32_MAX ? INT32_MAX : (int32_t)v;
+}
 
 // The largest s < n with v[s] <= i (v[0] <= i).
 __device__ __forceinline__ int last_at_most(const int32_t* v, int n, int64_t i) {
@@ -32,7 +40,7 @@ __device__ __forceinline__ int last_at_most(const int32_t* v, int n, int64_t i) 
   return lo;
 }
 
-__global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a, int per) {
+__global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a, int per, int rows, Div page) {
   extern __shared__ int32_t lds[];  // starts [S + 1], first page taken [S + 1]
   __shared__ int32_t wave[2][kPlanThreads / 64];
   int32_t* starts = lds;
@@ -43,8 +51,8 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a, in
   int32_t nt = 0, np = 0;
 #pragma unroll 4
   for (int s = s0; s < s1; ++s) {
-    const int32_t c = a.cached[s] < 0 ? 0 : a.cached[s], n = a.fresh[s] < 0 ? 0 : a.fresh[s];
-    const int32_t p = pages_of((int64_t)c + n, a.page_size) - pages_of(c, a.page_size);
+    const int32_t c = length_of(a.cached, s), n = length_of(a.fresh, s);
+    const int32_t p = pages_of(clamped_sum(c, n), page) - pages_of(c, page);
     starts[s] = n, first[s] = p;
     nt += n, np += p;
   }
@@ -75,39 +83,41 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a, in
   const int64_t gsz = (int64_t)gridDim.x * kPlanThreads;
   for (int64_t s = gid; s <= a.S; s += gsz) {
     a.starts[s] = starts[s];
-    if (s < a.S) a.total[s] = (a.cached[s] < 0 ? 0 : a.cached[s]) + starts[s + 1] - starts[s];
+    if (s < a.S) a.total[s] = clamped_sum(length_of(a.cached, s), starts[s + 1] - starts[s]);
   }
   if (gid == 0) *a.pages_needed = run_p;
   // new table entries, in the order of the free list
   for (int64_t i = gid; i < run_p; i += gsz) {
     const int q = last_at_most(first, a.S, i);
-    const int64_t col = pages_of(a.cached[q] < 0 ? 0 : a.cached[q], a.page_size) + (i - first[q]);
+    const int64_t col = (int64_t)pages_of(length_of(a.cached, q), page) + (i - first[q]);
     if (col < a.table_cols) a.table[q * a.table_cols + col] = i < a.n_free ? a.free_pages[i] : -1;
   }
-  // rows: a thread takes four in a row, searches for the first one's sequence
-  // and walks on from there
-  for (int64_t t0 = 4 * gid; t0 < a.T; t0 += 4 * gsz) {
+  // token rows: a thread takes `rows` in a row, searches for the first one's
+  // sequence and walks on from there
+  for (int64_t t0 = rows * gid; t0 < a.T; t0 += rows * gsz) {
     int q = t0 < run_t ? last_at_most(starts, a.S, t0) : 0;
-    for (int64_t t = t0; t < t0 + 4 && t < a.T; ++t) {
+    for (int64_t t = t0; t < t0 + rows && t < a.T; ++t) {
       int32_t slot = -1;
       int64_t pos = 0;
       if (t < run_t) {
         while (starts[q + 1] <= t) ++q;  // t < starts[S]
-        const int32_t c = a.cached[q] < 0 ? 0 : a.cached[q];
+        const int32_t c = length_of(a.cached, q);
         pos = c + (t - starts[q]);
-        const int64_t col = pos / a.page_size, have = pages_of(c, a.page_size);
-        int32_t page = -1;
-        if (col < a.table_cols) {
-          if (col < have) {
-            page = a.table[q * a.table_cols + col];
-          } else {
-            const int64_t i = first[q] + col - have;
-            if (i < a.n_free) page = a.free_pages[i];
+        if (pos <= INT32_MAX) {
+          const int32_t col = (int32_t)pos / page, have = pages_of(c, page);
+          int32_t pg = -1;
+          if (col < a.table_cols) {
+            if (col < have) {
+              pg = a.table[q * a.table_cols + col];
+            } else {
+              const int64_t i = (int64_t)first[q] + col - have;
+              if (i < a.n_free) pg = a.free_pages[i];
+            }
           }
-        }
-        if (page >= 0) {
-          const int64_t v = (int64_t)page * a.page_size + pos % a.page_size;
-          slot = v < ((int64_t)1 << 31) ? (int32_t)v : -1;
+          if (pg >= 0) {
+            const int64_t v = (int64_t)pg * a.page_size + ((int32_t)pos - col * a.page_size);
+            if (v <= INT32_MAX) slot = (int32_t)v;
+          }
         }
       }
       a.slots[t] = slot;
@@ -119,10 +129,13 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a, in
 }  // namespace
 
 hipError_t launch_paged_plan(const PlanArgs& a, hipStream_t stream) {
-  int64_t wgs = (a.T + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+  // a row per thread while that takes no more workgroups than CUs
+  const int rows = a.T <= 256 * kPlanThreads ? 1 : 4;
+  int64_t wgs = (a.T + rows * kPlanThreads - 1) / (rows * kPlanThreads);
   wgs = wgs < 1 ? 1 : wgs > 256 ? 256 : wgs;
   hipLaunchKernelGGL(paged_plan_kernel, dim3((unsigned)wgs), dim3(kPlanThreads),
-                     2 * (size_t)(a.S + 1) * sizeof(int32_t), stream, a, (a.S + kPlanThreads - 1) / kPlanThreads);
+                     2 * (size_t)(a.S + 1) * sizeof(int32_t), stream, a, (a.S + kPlanThreads - 1) / kPlanThreads,
+                     rows, div_by((uint32_t)a.page_size));
   return hipGetLastError();
 }
 

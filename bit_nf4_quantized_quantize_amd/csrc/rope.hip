@@ -64,22 +64,6 @@ __device__ __forceinline__ T* cache_row(void* cache, int32_t slot, int head, con
   return (T*)cache + (((page * a.kv_heads + head) << a.page_shift) + off) * (int64_t)a.head_dim;
 }
 
-// n / d for n < 2^31 by one multiplication (Granlund and Montgomery, "Division
-// by invariant integers using multiplication", PLDI 1994).
-struct Div {
-  uint32_t mul, d;
-  int shift;
-};
-Div div_by(uint32_t d) {
-  Div v = {0, d, 0};
-  while (((uint64_t)1 << v.shift) < d) ++v.shift;
-  v.mul = (uint32_t)(((((uint64_t)1 << v.shift) - d) << 32) / d + 1);
-  return v;
-}
-__device__ __forceinline__ int operator/(int n, const Div& v) {
-  return (int)((__umulhi((uint32_t)n, v.mul) + (uint32_t)n) >> v.shift);
-}
-
 // One piece of work: 16 bytes of one head (of each half of its pairs).
 template <typename T, int EV>
 struct Unit {

@@ -101,9 +101,10 @@ struct AttnArgs {
   float* part_ml;  // [S][q_heads][splits][2]: maximum (base-2 scores) and sum
   int64_t q_stride, S, num_pages, table_cols;
   int q_heads, kv_heads, head_dim, page_shift, splits;
+  int waves;       // per workgroup, set by the launcher
   float scale;
 };
-int paged_splits(int64_t S, int q_heads, int kv_heads, int64_t max_len);
+int paged_splits(int64_t S, int q_heads, int kv_heads, int head_dim, int64_t max_len);
 hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t stream);
 
 }  // namespace qlora

@@ -317,7 +317,7 @@ int qlora_paged_attention_workspace(int64_t S, int32_t q_heads, int32_t kv_heads
   int st;
   if ((st = check_attention(S, q_heads, kv_heads, head_dim, table_cols, page_size, fn))) return st;
   if (!ws_bytes) return fail(QLORA_ERR_INVALID_ARG, "%s: ws_bytes is NULL", fn);
-  const int splits = paged_splits(S, q_heads, kv_heads, table_cols * page_size);
+  const int splits = paged_splits(S, q_heads, kv_heads, head_dim, table_cols * page_size);
   *ws_bytes = splits > 1 ? S * q_heads * splits * (int64_t)(head_dim + 2) * 4 : 0;
   return QLORA_OK;
 }
@@ -339,7 +339,7 @@ int qlora_paged_attention(const void* q, int64_t q_stride, int64_t S, int32_t q_
       (lse && (st = check_ptr(lse, "lse", fn, 4))))
     return st;
   AttnArgs a = {};
-  a.splits = paged_splits(S, q_heads, kv_heads, table_cols * page_size);
+  a.splits = paged_splits(S, q_heads, kv_heads, head_dim, table_cols * page_size);
   if (a.splits > 1) {
     const int64_t rows = S * q_heads * a.splits, need = rows * (int64_t)(head_dim + 2) * 4;
     if (ws_bytes < need)

@@ -161,17 +161,16 @@ hipError_t launch_paged_plan(const PlanArgs& a, hipStream_t stream) {
 namespace {
 
 constexpr int kTile = 32;      // tokens per wave and step
-constexpr int kAttnWaves = 4;
 
 // How a sequence of n tokens is cut: `parts` ranges of `per` tiles (the last
 // may be shorter).  No range is shorter than one tile per wave.
 struct Cut {
   int64_t tiles, per, parts;
 };
-__device__ __forceinline__ Cut cut_of(int64_t n, int splits) {
+__device__ __forceinline__ Cut cut_of(int64_t n, int splits, int waves) {
   Cut c;
   c.tiles = (n + kTile - 1) / kTile;
-  int64_t most = (c.tiles + kAttnWaves - 1) / kAttnWaves;
+  int64_t most = (c.tiles + waves - 1) / waves;
   if (most > splits) most = splits;
   if (most < 1) most = 1;
   c.per = (c.tiles + most - 1) / most;
@@ -225,15 +224,15 @@ __device__ __forceinline__ void load_tile(Tile<DP>& t, const AttnArgs& a, const 
   }
 }
 
-template <int DP>
-__global__ __launch_bounds__(64 * kAttnWaves) void paged_attention_kernel(AttnArgs a, int qtiles) {
+template <int DP, int W>
+__global__ __launch_bounds__(64 * W) void paged_attention_kernel(AttnArgs a, int qtiles) {
   constexpr int CH = DP / 8;
   constexpr int PITCH = DP + 16;  // of the V tile: 16 rows of one column go to different banks
   constexpr int OP = DP + 4;      // of the partial outputs
   constexpr int WAVE_BYTES = kTile * PITCH * 2;
   static_assert(16 * OP * 4 <= WAVE_BYTES, "a wave's outputs take the place of its V tile");
-  __shared__ __attribute__((aligned(16))) char lds[kAttnWaves * WAVE_BYTES];
-  __shared__ float s_m[kAttnWaves][16], s_l[kAttnWaves][16];
+  __shared__ __attribute__((aligned(16))) char lds[W * WAVE_BYTES];
+  __shared__ float s_m[W][16], s_l[W][16];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, col = lane & 15, d = a.head_dim;
@@ -245,7 +244,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void paged_attention_kernel(AttnAr
   const int group = a.q_heads / a.kv_heads;
   const int h0 = kv * group + qt * 16, heads = group - qt * 16 < 16 ? group - qt * 16 : 16;
   const int64_t n = tokens_of(a, s);
-  const Cut cut = cut_of(n, a.splits);
+  const Cut cut = cut_of(n, a.splits, W);
   if (a.splits > 1 && z >= cut.parts) return;
   const int64_t first = z * cut.per;
   const int64_t last = first + cut.per < cut.tiles ? first + cut.per : cut.tiles;
@@ -271,7 +270,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void paged_attention_kernel(AttnAr
   Tile<DP> t;
   int64_t ti = first + wave;
   if (ti < last) load_tile<DP>(t, a, table, ti * kTile, n, kv, lane);
-  for (; ti < last; ti += kAttnWaves) {
+  for (; ti < last; ti += W) {
     const int64_t tok = ti * kTile;
     const bool full = tok + kTile <= n && t.ok[0] && t.ok[1];
     // V to LDS
@@ -296,7 +295,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void paged_attention_kernel(AttnAr
       }
     }
     const bool ok0 = t.ok[0], ok1 = t.ok[1];
-    if (ti + kAttnWaves < last) load_tile<DP>(t, a, table, tok + kAttnWaves * kTile, n, kv, lane);
+    if (ti + W < last) load_tile<DP>(t, a, table, tok + W * kTile, n, kv, lane);
     float p[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) p[j] = sc[j >> 2][j & 3] * scale2;
@@ -344,16 +343,16 @@ __global__ __launch_bounds__(64 * kAttnWaves) void paged_attention_kernel(AttnAr
 #pragma unroll
   for (int i = 0; i < DP / 16; ++i) *reinterpret_cast<floatx4*>(ow + col * OP + 16 * i + 4 * g) = acc[i];
   __syncthreads();
-  for (int e = threadIdx.x; e < heads * (d / 4); e += 64 * kAttnWaves) {
+  for (int e = threadIdx.x; e < heads * (d / 4); e += 64 * W) {
     const int h = e / (d / 4), c = e % (d / 4) * 4;
     float mx = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) mx = fmaxf(mx, s_m[w][h]);
+    for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_m[w][h]);
     const float mu = mx == -INFINITY ? 0.0f : mx;
     float sum = 0.0f;
     floatx4 o = {0, 0, 0, 0};
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) {
+    for (int w = 0; w < W; ++w) {
       const float f = __builtin_amdgcn_exp2f(s_m[w][h] - mu);
       sum += s_l[w][h] * f;
       o += *reinterpret_cast<const floatx4*>(reinterpret_cast<const float*>(lds + w * WAVE_BYTES) + h * OP + c) * f;
@@ -380,7 +379,7 @@ __global__ __launch_bounds__(256) void paged_join_kernel(AttnArgs a) {
   __shared__ floatx4 s_o[256];
   const int64_t s = blockIdx.y, row = s * a.q_heads + blockIdx.x;
   const int d = a.head_dim, dq = d / 4, t = threadIdx.x;
-  const int parts = (int)cut_of(tokens_of(a, s), a.splits).parts;
+  const int parts = (int)cut_of(tokens_of(a, s), a.splits, a.waves).parts;
   if (t < 64) {
     float m = -INFINITY, l = 0.0f;
     if (t < parts) {
@@ -415,31 +414,51 @@ __global__ __launch_bounds__(256) void paged_join_kernel(AttnArgs a) {
   }
 }
 
-template <int DP>
+template <int DP, int W>
 void attention_as(const AttnArgs& a, hipStream_t stream) {
   const int qtiles = (a.q_heads / a.kv_heads + 15) / 16;
-  hipLaunchKernelGGL(paged_attention_kernel<DP>, dim3((unsigned)(a.kv_heads * qtiles * a.splits), (unsigned)a.S),
-                     dim3(64 * kAttnWaves), 0, stream, a, qtiles);
+  hipLaunchKernelGGL((paged_attention_kernel<DP, W>), dim3((unsigned)(a.kv_heads * qtiles * a.splits), (unsigned)a.S),
+                     dim3(64 * W), 0, stream, a, qtiles);
+}
+
+template <int DP>
+void attention_waves(const AttnArgs& a, hipStream_t stream) {
+  if (a.waves == 8) attention_as<DP, 8>(a, stream);
+  else attention_as<DP, 4>(a, stream);
 }
 
 }  // namespace
 
-// Enough workgroups for 8 per CU, as far as the length gives each wave a tile.
-int paged_splits(int64_t S, int q_heads, int kv_heads, int64_t max_len) {
-  if (S == 0) return 1;
+// Eight waves per workgroup where the table can hold sequences of more than
+// 1024 tokens, else four: short sequences leave the waves behind the last tile
+// idle (64 sequences of 1 to 512 tokens, 32 heads of 128: 53 us with four, 63
+// with eight), long ones read a little faster with fewer, longer streams (64
+// of 1 to 2048: 206 and 194 us; 8 of 32768 to 65536, 8 kv heads: 293 and 283).
+// Heads of more than 128 keep four: eight waves' registers and V tiles would
+// leave a CU nothing else.
+static int waves_for(int head_dim, int64_t max_len) { return max_len > 1024 && head_dim <= 128 ? 8 : 4; }
+
+// No split up to 512 tokens, where one launch takes less than two (1 sequence
+// of 512, 32 heads: 9.5 us against 14); else enough workgroups for four per
+// CU, as far as the length gives each wave a tile.
+int paged_splits(int64_t S, int q_heads, int kv_heads, int head_dim, int64_t max_len) {
+  if (S == 0 || max_len <= 512) return 1;
+  const int waves = waves_for(head_dim, max_len);
   const int64_t wgs = S * kv_heads * ((q_heads / kv_heads + 15) / 16);
-  int64_t n = (8 * 256 + wgs - 1) / wgs;
-  const int64_t most = (max_len + kAttnWaves * kTile - 1) / (kAttnWaves * kTile);
+  int64_t n = (4 * 256 * (8 / waves) + wgs - 1) / wgs;
+  const int64_t most = (max_len + waves * kTile - 1) / (waves * kTile);
   if (n > most) n = most;
   if (n > kMaxSplits) n = kMaxSplits;
   return n < 1 ? 1 : (int)n;
 }
 
-hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t stream) {
-  if (a.head_dim <= 64) attention_as<64>(a, stream);
-  else if (a.head_dim <= 96) attention_as<96>(a, stream);
-  else if (a.head_dim <= 128) attention_as<128>(a, stream);
-  else attention_as<256>(a, stream);
+hipError_t launch_paged_attention(const AttnArgs& args, hipStream_t stream) {
+  AttnArgs a = args;
+  a.waves = waves_for(a.head_dim, a.table_cols << a.page_shift);
+  if (a.head_dim <= 64) attention_waves<64>(a, stream);
+  else if (a.head_dim <= 96) attention_waves<96>(a, stream);
+  else if (a.head_dim <= 128) attention_waves<128>(a, stream);
+  else attention_as<256, 4>(a, stream);
   if (a.splits > 1)
     hipLaunchKernelGGL(paged_join_kernel, dim3(a.q_heads, (unsigned)a.S), dim3(256), 0, stream, a);
   return hipGetLastError();

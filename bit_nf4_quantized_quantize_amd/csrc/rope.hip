@@ -39,8 +39,16 @@ struct alignas(EV * sizeof(T)) Piece {
 
 template <typename T, int EV>
 __device__ __forceinline__ Piece<T, EV> ld(const T* p) { return *reinterpret_cast<const Piece<T, EV>*>(p); }
-template <typename T, int EV>
-__device__ __forceinline__ void st(T* p, const Piece<T, EV>& v) { *reinterpret_cast<Piece<T, EV>*>(p) = v; }
+// PAST: 16-byte stores that do not stay in the L2.
+template <typename T, int EV, bool PAST>
+__device__ __forceinline__ void st(T* p, const Piece<T, EV>& v) {
+  if constexpr (PAST && EV > 1) {
+    typedef uint32_t words __attribute__((ext_vector_type(4)));
+    __builtin_nontemporal_store(__builtin_bit_cast(words, v), reinterpret_cast<words*>(p));
+  } else {
+    *reinterpret_cast<Piece<T, EV>*>(p) = v;
+  }
+}
 
 // cos and sin of 2 pi pos turns, times mscale.  The remainder that fp32 drops
 // from the reduced angle is put back to first order.
@@ -78,7 +86,7 @@ struct Unit {
 // of the rest of the head; the values' heads are pieces throughout.
 // blockIdx.y takes a share of a token group's units.  A thread loads UN units
 // before it stores the first.
-template <typename T, int EV, bool INTER, int UN>
+template <typename T, int EV, bool INTER, bool PAST, int UN>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, int nt, Div by_units, Div by_hu, Div by_vu,
                                                         Div by_half) {
   extern __shared__ float trig[];  // [nt][half] cosines, then as many sines
@@ -163,25 +171,32 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, int nt, Div 
           }
         }
       }
-      st<T, EV>(w[j].dst + w[j].a, w[j].x);
-      if (w[j].b >= 0) st<T, EV>(w[j].dst + w[j].b, w[j].y);
+      st<T, EV, PAST>(w[j].dst + w[j].a, w[j].x);
+      if (w[j].b >= 0) st<T, EV, PAST>(w[j].dst + w[j].b, w[j].y);
     }
   }
 }
 
 template <typename T, int EV, bool INTER>
 hipError_t rope_as(const RopeArgs& a, hipStream_t stream) {
-  // Few tokens: one token per workgroup and its units over several; many: four
-  // tokens share a workgroup.
-  const int nt = a.T >= 1024 ? 4 : 1;
-  const int64_t gx = (a.T + nt - 1) / nt;
-  const unsigned gy = gx >= 512 ? 1 : 4;
   const int half = a.rot_dim / 2, pe = INTER ? (EV > 1 ? EV / 2 : 1) : EV;
   const int hu = half / pe + (a.head_dim - a.rot_dim) / EV, vu = a.head_dim / EV;
   const int units = (a.q_heads + a.kv_heads) * hu + (a.v ? a.kv_heads * vu : 0);
+  // Tokens per workgroup: about 2048 units, up to 4 tokens (8191 tokens of 72
+  // heads of 128 in fp32, 2304 units each: 113 us with one token, 127 with two,
+  // 149 with four; 4096 tokens of 64 heads in bf16, 512 units each: 24.3, 22.5,
+  // 23.5).  Few tokens: the units of one token over four workgroups.
+  int nt = 2048 / units;
+  nt = a.T < 1024 || nt < 1 ? 1 : nt > 4 ? 4 : nt;
+  const int64_t gx = (a.T + nt - 1) / nt;
+  const unsigned gy = gx >= 512 ? 1 : 4;
   const size_t lds = (size_t)nt * a.rot_dim * sizeof(float);
-  hipLaunchKernelGGL((rope_kernel<T, EV, INTER, 4>), dim3((unsigned)gx, gy), dim3(kThreads), lds, stream, a, nt,
-                     div_by(units), div_by(hu), div_by(vu), div_by(half ? half : 1));
+  // More than the L2 holds goes past it (8192 tokens of 32 heads to the cache:
+  // 79 us against 85; 4096 rotated: 21.9 and 23.5).
+  const int64_t bytes = a.T * ((int64_t)a.q_heads + (a.v ? 2 : 1) * a.kv_heads) * a.head_dim * (int64_t)sizeof(T);
+  const auto kernel = bytes > ((int64_t)32 << 20) ? rope_kernel<T, EV, INTER, true, 4> : rope_kernel<T, EV, INTER, false, 4>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)gx, gy), dim3(kThreads), lds, stream, a, nt, div_by(units), div_by(hu),
+                     div_by(vu), div_by(half ? half : 1));
   return hipGetLastError();
 }
 

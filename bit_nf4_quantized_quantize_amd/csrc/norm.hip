@@ -4,9 +4,8 @@
 // Both directions are streams over rows of D elements with one or two row
 // means in between, bound by HBM: the forward reads x and h and writes xo and
 // n once, the backward reads dxo, xo, dn and h and writes dx and dh once.  A
-// row is held in the registers of its threads (TPR threads, NV chunks of 8
-// elements each), so nothing is read twice; rows of up to 512 x 2 elements
-// take one wave, wider ones a workgroup.
+// row is held in the registers of its threads (NV chunks of 8 elements each), so nothing is read twice; 512 elements
+// to a wave (1024 beyond 8192).
 #include "decoder.h"
 #include "device.h"
 
@@ -23,88 +22,60 @@ struct Raw8<uint16_t> {
   __device__ __forceinline__ float get(int i) const {
     return __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
   }
+  __device__ __forceinline__ void set(int i, uint16_t e) { w[i >> 1] |= (uint32_t)e << (16 * (i & 1)); }
+  static __device__ __forceinline__ Raw8 of(const float (&v)[8]) {
+    return {{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7])}};
+  }
+  __device__ __forceinline__ uint16_t elem(int i) const { return (uint16_t)(w[i >> 1] >> (16 * (i & 1))); }
 };
 template <>
 struct Raw8<float> {
   float v[8];
   __device__ __forceinline__ float get(int i) const { return v[i]; }
+  __device__ __forceinline__ void set(int i, float e) { v[i] = e; }
+  static __device__ __forceinline__ Raw8 of(const float (&v)[8]) {
+    return {{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]}};
+  }
+  __device__ __forceinline__ float elem(int i) const { return v[i]; }
 };
 
-__device__ __forceinline__ void put(uint16_t* p, float v) { *p = f2bf(v); }
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+// Elements j .. j + 7 of a row of D (those that exist; the rest reads as zero
+// and is not written).  ALIGNED: D % 8 == 0, so the pieces of every row lie on
+// 16-byte boundaries and are there whole or not at all; otherwise they are
+// moved with the same 16-byte accesses at element alignment, which global
+// memory allows, and the row's last piece element by element (8000 rows of
+// 4097 forward: 211 us with element accesses throughout).
+template <bool ALIGNED, typename T>
+__device__ __forceinline__ Raw8<T> load8(const T* row, int j, int D) {
+  Raw8<T> r = {};
+  if (ALIGNED) {
+    if (j < D) r = *reinterpret_cast<const Raw8<T>*>(__builtin_assume_aligned(row + j, 16));
+  } else if (j + 8 <= D) {
+    __builtin_memcpy(&r, row + j, sizeof(r));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (j + i < D) r.set(i, row[j + i]);
+  }
+  return r;
+}
+template <bool ALIGNED, typename T>
+__device__ __forceinline__ void store8(T* row, const float (&v)[8], int j, int D) {
+  const Raw8<T> r = Raw8<T>::of(v);
+  if (ALIGNED) {
+    if (j < D) *reinterpret_cast<Raw8<T>*>(__builtin_assume_aligned(row + j, 16)) = r;
+  } else if (j + 8 <= D) {
+    __builtin_memcpy(row + j, &r, sizeof(r));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (j + i < D) row[j + i] = r.elem(i);
+  }
+}
 
-// How a thread's chunk c maps to elements of its row.  VEC (D % 8 == 0, so
-// every row starts 16-byte aligned): 8 consecutive elements; otherwise
-// element by element, consecutive threads on consecutive elements.
-template <int TPR, bool VEC>
-struct Map {
-  static __device__ __forceinline__ int at(int c, int i, int t) {
-    return VEC ? (c * TPR + t) * 8 + i : (c * 8 + i) * TPR + t;
-  }
-  static __device__ __forceinline__ Raw8<uint16_t> load(const uint16_t* row, int c, int t, int D) {
-    Raw8<uint16_t> r = {{0, 0, 0, 0}};
-    if (VEC) {
-      const int j = at(c, 0, t);
-      if (j < D) {
-        const uint4 q = *reinterpret_cast<const uint4*>(row + j);
-        r.w[0] = q.x, r.w[1] = q.y, r.w[2] = q.z, r.w[3] = q.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int j = at(c, i, t);
-        const uint32_t e = j < D ? row[j] : 0;
-        r.w[i >> 1] |= e << (16 * (i & 1));
-      }
-    }
-    return r;
-  }
-  static __device__ __forceinline__ Raw8<float> load(const float* row, int c, int t, int D) {
-    Raw8<float> r;
-    if (VEC) {
-      const int j = at(c, 0, t);
-      float4 a = make_float4(0, 0, 0, 0), b = a;
-      if (j < D) {
-        a = *reinterpret_cast<const float4*>(row + j);
-        b = *reinterpret_cast<const float4*>(row + j + 4);
-      }
-      r.v[0] = a.x, r.v[1] = a.y, r.v[2] = a.z, r.v[3] = a.w;
-      r.v[4] = b.x, r.v[5] = b.y, r.v[6] = b.z, r.v[7] = b.w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int j = at(c, i, t);
-        r.v[i] = j < D ? row[j] : 0.0f;
-      }
-    }
-    return r;
-  }
-  static __device__ __forceinline__ void store(uint16_t* row, const float (&v)[8], int c, int t, int D) {
-    if (VEC) {
-      const int j = at(c, 0, t);
-      if (j < D)
-        *reinterpret_cast<uint4*>(row + j) =
-            make_uint4(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (at(c, i, t) < D) put(row + at(c, i, t), v[i]);
-    }
-  }
-  static __device__ __forceinline__ void store(float* row, const float (&v)[8], int c, int t, int D) {
-    if (VEC) {
-      const int j = at(c, 0, t);
-      if (j < D) {
-        *reinterpret_cast<float4*>(row + j) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4*>(row + j + 4) = make_float4(v[4], v[5], v[6], v[7]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (at(c, i, t) < D) put(row + at(c, i, t), v[i]);
-    }
-  }
-};
+// A value that is the same in all lanes of a wave, as the compiler is to see
+// it: row addresses made from it stay in scalar registers.
+__device__ __forceinline__ int wave_uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 template <int S>
 __device__ __forceinline__ float dpp_ror(float v) {
@@ -131,69 +102,74 @@ __device__ __forceinline__ void wave_sum(float (&v)[N]) {
   }
 }
 
-// Sums over the TPR threads of a row.  `buf` holds two sets of wave sums used
-// in turn, so one barrier per sum suffices: a set is written again only after
-// the barrier of the sum in between, which every thread passes after it has
-// read the set.
-template <int TPR, int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float (*buf)[3][16], int& turn) {
+// Sums over the `tpr` threads of a row (a multiple of 64, at most 1024; the
+// rows of a workgroup take theirs together).  `buf` holds two sets of wave sums
+// used in turn, so one barrier per sum suffices: a set is written again only
+// after the barrier of the sum in between, which every thread passes after it
+// has read the set.
+template <int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float (*buf)[3][16], int& turn, int tpr) {
   wave_sum<N>(v);
-  if (TPR == 64) return;
+  if (tpr == 64) return;
   float(*s)[16] = buf[turn];
   turn ^= 1;
+  const int wave = threadIdx.x >> 6, waves = tpr >> 6, first = wave / waves * waves;
   if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) s[k][threadIdx.x >> 6] = v[k];
+    for (int k = 0; k < N; ++k) s[k][wave] = v[k];
   }
   __syncthreads();
+  // lane i of 16 takes the sum of the row's wave i; rotations add them
+  const int i = threadIdx.x & 15;
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    float t = 0.0f;
-#pragma unroll
-    for (int w = 0; w < TPR / 64; ++w) t += s[k][w];
+    float t = i < waves ? s[k][first + i] : 0.0f;
+    t += dpp_ror<1>(t);
+    t += dpp_ror<2>(t);
+    t += dpp_ror<4>(t);
+    t += dpp_ror<8>(t);
     v[k] = t;
   }
 }
 
-constexpr int wg_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
-
-template <typename XT, typename HT, int TPR, int NV, bool VEC>
-__global__ __launch_bounds__(wg_threads(TPR)) void norm_fwd_kernel(NormArgs a) {
-  using M = Map<TPR, VEC>;
+// A row per workgroup of tpr threads, or four rows of one wave each (rows of
+// one workgroup end at different times, which only waves may).
+template <typename XT, typename HT, int NV, bool AL>
+__global__ __launch_bounds__(1024, NV == 1 ? 8 : 4) void norm_fwd_kernel(NormArgs a, int tpr) {
   __shared__ float buf[2][3][16];
-  constexpr int ROWS = wg_threads(TPR) / TPR;
-  const int t = threadIdx.x % TPR, D = a.D;
+  const int rows = tpr == 64 ? 4 : 1, sub = tpr == 64 ? wave_uniform(threadIdx.x >> 6) : 0;
+  const int t = threadIdx.x - sub * tpr, D = a.D;
   const float inv = 1.0f / (float)D;
   int turn = 0;
-  for (int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR; r < a.T; r += (int64_t)gridDim.x * ROWS) {
+  for (int64_t r = (int64_t)blockIdx.x * rows + sub; r < a.T; r += (int64_t)gridDim.x * rows) {
     float x[NV][8];
-    const XT* xr = (const XT*)a.x + r * D;
+    Raw8<XT> rx[NV];
+    Raw8<HT> h[NV];
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      const auto v = M::load(xr, c, t, D);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[c][i] = v.get(i);
+      rx[c] = load8<AL>((const XT*)a.x + r * D, (c * tpr + t) * 8, D);
+      if (a.h) h[c] = load8<AL>((const HT*)a.h + r * D, (c * tpr + t) * 8, D);
     }
-    if (a.h) {
-      Raw8<HT> h[NV];
-      const HT* hr = (const HT*)a.h + r * D;
-      float s[1] = {0.0f};
 #pragma unroll
-      for (int c = 0; c < NV; ++c) h[c] = M::load(hr, c, t, D);
+    for (int c = 0; c < NV; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[c][i] = rx[c].get(i);
+    if (a.h) {
+      float s[1] = {0.0f};
       float k = a.alpha;
       if (a.w_post) {
 #pragma unroll
         for (int c = 0; c < NV; ++c)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s[0] += h[c].get(i) * h[c].get(i);
-        row_sum<TPR, 1>(s, buf, turn);
+          for (int i = 0; i < 8; ++i) s[0] = __builtin_fmaf(h[c].get(i), h[c].get(i), s[0]);
+        row_sum<1>(s, buf, turn, tpr);
         k *= 1.0f / sqrtf(s[0] * inv + a.eps);
       }
 #pragma unroll
       for (int c = 0; c < NV; ++c) {
         Raw8<float> w, g;
-        if (a.w_post) w = M::load(a.w_post, c, t, D);
-        if (a.gate) g = M::load(a.gate, c, t, D);
+        if (a.w_post) w = load8<AL>(a.w_post, (c * tpr + t) * 8, D);
+        if (a.gate) g = load8<AL>(a.gate, (c * tpr + t) * 8, D);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float u = h[c].get(i) * k;
@@ -204,40 +180,54 @@ __global__ __launch_bounds__(wg_threads(TPR)) void norm_fwd_kernel(NormArgs a) {
       }
     }
     if (a.xo) {
-      XT* o = (XT*)a.xo + r * D;
 #pragma unroll
-      for (int c = 0; c < NV; ++c) M::store(o, x[c], c, t, D);
+      for (int c = 0; c < NV; ++c) store8<AL>((XT*)a.xo + r * D, x[c], (c * tpr + t) * 8, D);
     }
     if (a.n) {
       float s[1] = {0.0f};
 #pragma unroll
       for (int c = 0; c < NV; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] += x[c][i] * x[c][i];
-      row_sum<TPR, 1>(s, buf, turn);
+        for (int i = 0; i < 8; ++i) s[0] = __builtin_fmaf(x[c][i], x[c][i], s[0]);
+      row_sum<1>(s, buf, turn, tpr);
       const float rs = 1.0f / sqrtf(s[0] * inv + a.eps);
-      HT* o = (HT*)a.n + r * D;
 #pragma unroll
       for (int c = 0; c < NV; ++c) {
-        const Raw8<float> w = M::load(a.w_pre, c, t, D);
+        const Raw8<float> w = load8<AL>(a.w_pre, (c * tpr + t) * 8, D);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[c][i] = x[c][i] * rs * w.get(i);
-        M::store(o, x[c], c, t, D);
+        store8<AL>((HT*)a.n + r * D, x[c], (c * tpr + t) * 8, D);
       }
     }
   }
 }
 
+// What a thread reads of one row in the backward.
+template <typename XT, typename HT, int NV>
+struct BwdRow {
+  Raw8<XT> xo[NV], dxo[NV];
+  Raw8<HT> dn[NV], h[NV];
+};
+
 // The backward of one row needs two rounds of row sums: first sum xo^2, sum a
-// xo (for dx) and sum h^2, then sum b w_post h (for dh).  SUMS: the sums over
-// tokens are kept in the thread's registers, one per element it owns, and
-// written once per workgroup row group; norm_sums_kernel adds those.
-template <typename XT, typename HT, int TPR, int NV, bool VEC, bool SUMS>
-__global__ __launch_bounds__(wg_threads(TPR)) void norm_bwd_kernel(NormArgs a, int64_t parts) {
-  using M = Map<TPR, VEC>;
+// xo (for dx) and sum h^2, then sum b w_post h (for dh).  One workgroup of up
+// to 1024 threads per CU walks over the rows, as many at a time as it holds, with the next rows'
+// loads in flight under the present ones' sums and barriers.  SUMS: the sums
+// over tokens are kept in the threads' registers, one per element a thread
+// owns, added over the workgroup's row groups in LDS at the end and written
+// once per workgroup; norm_sums_kernel adds those.  The gains lie in LDS for the
+// whole walk: registers have no room for them beside the sums, the row and the
+// next row, and from the L2 they would double its reads.  Rows beyond 8192
+// (NV = 2) have no room for either, and no next row in flight.
+constexpr int kBwdThreads = 1024;
+
+template <typename XT, typename HT, int NV, bool AL, bool SUMS>
+__global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs a, int tpr, int rows) {
   __shared__ float buf[2][3][16];
-  constexpr int ROWS = wg_threads(TPR) / TPR;
-  const int t = threadIdx.x % TPR, D = a.D;
+  extern __shared__ __attribute__((aligned(16))) float lds[];  // the gains, at the end the row groups' sums
+  constexpr bool LDS_GAINS = NV == 1, AHEAD = NV == 1;
+  using Row = BwdRow<XT, HT, NV>;
+  const int sub = wave_uniform(threadIdx.x / tpr), t = threadIdx.x - sub * tpr, D = a.D;
   const float inv = 1.0f / (float)D;
   int turn = 0;
   float sp[NV][8], sg[NV][8], sw[NV][8];
@@ -247,89 +237,142 @@ __global__ __launch_bounds__(wg_threads(TPR)) void norm_bwd_kernel(NormArgs a, i
 #pragma unroll
       for (int i = 0; i < 8; ++i) sp[c][i] = sg[c][i] = sw[c][i] = 0.0f;
   }
-  const int64_t first = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
-  for (int64_t r = first; r < a.T; r += (int64_t)gridDim.x * ROWS) {
-    Raw8<XT> xo[NV], dxo[NV];
-    Raw8<HT> dn[NV], h[NV];
+  auto load = [&](Row& w, int64_t r) {
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      xo[c] = M::load((const XT*)a.x + r * D, c, t, D);
-      if (a.dxo) dxo[c] = M::load((const XT*)a.dxo + r * D, c, t, D);
-      if (a.dn) dn[c] = M::load((const HT*)a.dn + r * D, c, t, D);
-      if (a.h) h[c] = M::load((const HT*)a.h + r * D, c, t, D);
+      const int j = (c * tpr + t) * 8;
+      w.xo[c] = load8<AL>((const XT*)a.x + r * D, j, D);
+      if (a.dxo) w.dxo[c] = load8<AL>((const XT*)a.dxo + r * D, j, D);
+      if (a.dn) w.dn[c] = load8<AL>((const HT*)a.dn + r * D, j, D);
+      if (a.h) w.h[c] = load8<AL>((const HT*)a.h + r * D, j, D);
     }
+  };
+  const float* const gains[3] = {a.w_pre, a.w_post, a.gate};
+  if (LDS_GAINS) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      if (!gains[k]) continue;
+      for (int i = threadIdx.x; i < tpr * 8; i += blockDim.x) lds[k * tpr * 8 + i] = i < D ? gains[k][i] : 0.0f;
+    }
+    __syncthreads();
+  }
+  auto gain = [&](int k, int c) {
+    Raw8<float> w;
+    if (LDS_GAINS) {
+      w = *reinterpret_cast<const Raw8<float>*>(lds + (k * tpr + t) * 8);
+    } else {
+      int j = (c * tpr + t) * 8;
+      asm volatile("" : "+v"(j));  // loaded again for every row, not kept in registers
+      w = load8<AL>(gains[k], j, D);
+    }
+    return w;
+  };
+  // every row group makes the same number of turns (barriers); a group whose
+  // rows have run out repeats the last row and keeps nothing of it
+  const int64_t step = (int64_t)gridDim.x * rows;
+  Row nx;
+  int64_t r0 = (int64_t)blockIdx.x * rows;
+  if (AHEAD) load(nx, r0 + sub < a.T ? r0 + sub : a.T - 1);
+  for (; r0 < a.T; r0 += step) {
+    const int64_t r = r0 + sub;
+    const bool mine = r < a.T;
+    if (!AHEAD) load(nx, mine ? r : a.T - 1);
+    const Row w = nx;
+    if (AHEAD && r0 + step < a.T) load(nx, r + step < a.T ? r + step : a.T - 1);
     float s[3] = {0.0f, 0.0f, 0.0f};  // xo^2, a xo, h^2
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
       if (a.dn) {
-        const Raw8<float> w = M::load(a.w_pre, c, t, D);
+        const Raw8<float> wp = gain(0, c);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float x = xo[c].get(i);
-          s[0] += x * x;
-          s[1] += dn[c].get(i) * w.get(i) * x;
+          const float x = w.xo[c].get(i);
+          s[0] = __builtin_fmaf(x, x, s[0]);
+          s[1] = __builtin_fmaf(w.dn[c].get(i) * wp.get(i), x, s[1]);
         }
       }
       if (a.w_post) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[2] += h[c].get(i) * h[c].get(i);
+        for (int i = 0; i < 8; ++i) s[2] = __builtin_fmaf(w.h[c].get(i), w.h[c].get(i), s[2]);
       }
     }
-    row_sum<TPR, 3>(s, buf, turn);
+    row_sum<3>(s, buf, turn, tpr);
     const float rs = 1.0f / sqrtf(s[0] * inv + a.eps);
     const float back = rs * rs * (s[1] * inv);
     const float rh = a.w_post ? 1.0f / sqrtf(s[2] * inv + a.eps) : 1.0f;
-    float g[NV][8];  // dx, then alpha * dx
+    float g[NV][8];  // dx, then the gradient of y
     float q[1] = {0.0f};
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
+      const int j = (c * tpr + t) * 8;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[c][i] = a.dxo ? dxo[c].get(i) : 0.0f;
+      for (int i = 0; i < 8; ++i) g[c][i] = a.dxo ? w.dxo[c].get(i) : 0.0f;
       if (a.dn) {
-        const Raw8<float> w = M::load(a.w_pre, c, t, D);
+        const Raw8<float> wp = gain(0, c);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float x = xo[c].get(i), d = dn[c].get(i);
-          g[c][i] += rs * (d * w.get(i) - x * back);
-          if (SUMS) sw[c][i] += d * (x * rs);
+          const float x = w.xo[c].get(i), d = w.dn[c].get(i);
+          g[c][i] = __builtin_fmaf(rs, __builtin_fmaf(d, wp.get(i), -(x * back)), g[c][i]);
+          if (SUMS && mine) sw[c][i] = __builtin_fmaf(d, x * rs, sw[c][i]);
         }
       }
-      M::store((XT*)a.xo + r * D, g[c], c, t, D);
+      if (mine) store8<AL>((XT*)a.xo + r * D, g[c], j, D);
       Raw8<float> wp, gt;
-      if (a.w_post) wp = M::load(a.w_post, c, t, D);
-      if (a.gate) gt = M::load(a.gate, c, t, D);
+      if (a.w_post) wp = gain(1, c);
+      if (a.gate) gt = gain(2, c);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float y = a.h ? h[c].get(i) * rh : 0.0f;
+        const float y = a.h ? w.h[c].get(i) * rh : 0.0f;
         float b = g[c][i] * a.alpha;
-        if (SUMS) sg[c][i] += b * (a.w_post ? y * wp.get(i) : y);
+        if (SUMS && mine) sg[c][i] = __builtin_fmaf(b, a.w_post ? y * wp.get(i) : y, sg[c][i]);
         if (a.gate) b *= gt.get(i);
-        if (SUMS) sp[c][i] += b * y;
+        if (SUMS && mine) sp[c][i] = __builtin_fmaf(b, y, sp[c][i]);
         if (a.w_post) b *= wp.get(i);
-        q[0] += b * y;
+        q[0] = __builtin_fmaf(b, y, q[0]);
         g[c][i] = b;
       }
     }
     if (a.n) {
       if (a.w_post) {
-        row_sum<TPR, 1>(q, buf, turn);
+        row_sum<1>(q, buf, turn, tpr);
         const float m = q[0] * inv;
 #pragma unroll
         for (int c = 0; c < NV; ++c)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) g[c][i] = rh * (g[c][i] - h[c].get(i) * rh * m);
+          for (int i = 0; i < 8; ++i) g[c][i] = rh * (g[c][i] - w.h[c].get(i) * rh * m);
       }
+      if (mine) {
 #pragma unroll
-      for (int c = 0; c < NV; ++c) M::store((HT*)a.n + r * D, g[c], c, t, D);
+        for (int c = 0; c < NV; ++c) store8<AL>((HT*)a.n + r * D, g[c], (c * tpr + t) * 8, D);
+      }
     }
   }
   if (SUMS) {
+    auto flush = [&](float (&v)[NV][8], int which) {
+      if (rows > 1) {  // add the row groups' sums, in order
+        __syncthreads();
 #pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      if (a.dw_post) M::store(a.part + (0 * parts + first) * D, sp[c], c, t, D);
-      if (a.dgate) M::store(a.part + (1 * parts + first) * D, sg[c], c, t, D);
-      if (a.dw_pre) M::store(a.part + (2 * parts + first) * D, sw[c], c, t, D);
-    }
+        for (int c = 0; c < NV; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) lds[((sub * NV + c) * 8 + i) * tpr + t] = v[c][i];
+        __syncthreads();
+        if (sub == 0) {
+          for (int k = 1; k < rows; ++k)
+#pragma unroll
+            for (int c = 0; c < NV; ++c)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[c][i] += lds[((k * NV + c) * 8 + i) * tpr + t];
+        }
+      }
+      if (sub == 0) {
+        float* row = a.part + ((int64_t)which * gridDim.x + blockIdx.x) * D;
+#pragma unroll
+        for (int c = 0; c < NV; ++c) store8<AL>(row, v[c], (c * tpr + t) * 8, D);
+      }
+    };
+    if (a.dw_post) flush(sp, 0);
+    if (a.dgate) flush(sg, 1);
+    if (a.dw_pre) flush(sw, 2);
   }
 }
 
@@ -364,72 +407,63 @@ __global__ __launch_bounds__(256) void norm_zero_sums_kernel(NormArgs a) {
   if (a.dw_pre) a.dw_pre[i] = 0.0f;
 }
 
-constexpr int kBwdGroups = 512;  // workgroups of the backward when it keeps sums
+// Threads per row: 8 elements each up to 8192, then 16.
+int row_threads(int64_t D) {
+  const int64_t each = D <= 8192 ? 512 : 1024;  // elements per wave
+  return (int)((D + each - 1) / each) * 64;
+}
 
-// Threads per row of the backward for width D (the forward takes the same).
-int row_threads(int64_t D) { return D <= 1024 ? 64 : D <= 2048 ? 256 : D <= 4096 ? 512 : 1024; }
+// How the backward walks: `rows` at a time per workgroup, `groups` workgroups
+// at most.  One workgroup of up to 1024 threads per CU; with many rows of up to
+// 4096, two of up to 512, whose barriers do not meet (8191 x 4096: 139 and 134
+// us; 8192 x 2048: 51 and 49; but twice the partial sums, 300 x 4096: 19.5 and
+// 23.6 us, so only from 8 rows per workgroup on).
+struct Walk {
+  int rows, groups;
+};
+Walk walk_of(int64_t T, int64_t D) {
+  const bool two = D <= 4096 && T >= 8 * 512;
+  return {(two ? 512 : kBwdThreads) / row_threads(D), two ? 512 : 256};
+}
 
-template <typename XT, typename HT, int TPR, int NV>
-hipError_t fwd_as(const NormArgs& a, hipStream_t stream) {
-  constexpr int ROWS = wg_threads(TPR) / TPR;
-  const int64_t need = (a.T + ROWS - 1) / ROWS;
+template <typename XT, typename HT>
+hipError_t fwd_types(const NormArgs& a, hipStream_t stream) {
+  const int tpr = row_threads(a.D), rows = tpr == 64 ? 4 : 1;
+  const int64_t need = (a.T + rows - 1) / rows;
   const unsigned grid = (unsigned)(need < 65536 ? need : 65536);
-  if (a.D % 8 == 0)
-    hipLaunchKernelGGL((norm_fwd_kernel<XT, HT, TPR, NV, true>), dim3(grid), dim3(wg_threads(TPR)), 0, stream, a);
-  else
-    hipLaunchKernelGGL((norm_fwd_kernel<XT, HT, TPR, NV, false>), dim3(grid), dim3(wg_threads(TPR)), 0, stream, a);
+  const bool al = a.D % 8 == 0;
+  const auto kernel = a.D <= 8192 ? (al ? norm_fwd_kernel<XT, HT, 1, true> : norm_fwd_kernel<XT, HT, 1, false>)
+                                  : (al ? norm_fwd_kernel<XT, HT, 2, true> : norm_fwd_kernel<XT, HT, 2, false>);
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(tpr * rows), 0, stream, a, tpr);
   return hipGetLastError();
 }
 
-template <typename XT, typename HT, int TPR, int NV>
+template <typename XT, typename HT, int NV, bool AL>
 hipError_t bwd_as(const NormArgs& a, hipStream_t stream) {
-  constexpr int ROWS = wg_threads(TPR) / TPR;
+  const int tpr = row_threads(a.D), rows = walk_of(a.T, a.D).rows;
   const int64_t parts = norm_bwd_parts(a.T, a.D);
-  const unsigned grid = (unsigned)(parts / ROWS);
-  const dim3 wg(wg_threads(TPR));
-  const bool vec = a.D % 8 == 0, sums = a.dw_post || a.dgate || a.dw_pre;
-  if (vec && sums)
-    hipLaunchKernelGGL((norm_bwd_kernel<XT, HT, TPR, NV, true, true>), dim3(grid), wg, 0, stream, a, parts);
-  else if (vec)
-    hipLaunchKernelGGL((norm_bwd_kernel<XT, HT, TPR, NV, true, false>), dim3(grid), wg, 0, stream, a, parts);
-  else if (sums)
-    hipLaunchKernelGGL((norm_bwd_kernel<XT, HT, TPR, NV, false, true>), dim3(grid), wg, 0, stream, a, parts);
-  else
-    hipLaunchKernelGGL((norm_bwd_kernel<XT, HT, TPR, NV, false, false>), dim3(grid), wg, 0, stream, a, parts);
+  const bool sums = a.dw_post || a.dgate || a.dw_pre;
+  const size_t gains = NV == 1 ? 3 * (size_t)tpr * 32 : 0, add = sums && rows > 1 ? (size_t)rows * tpr * NV * 32 : 0;
+  const auto kernel = sums ? norm_bwd_kernel<XT, HT, NV, AL, true> : norm_bwd_kernel<XT, HT, NV, AL, false>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)parts), dim3(tpr * rows), gains > add ? gains : add, stream, a, tpr, rows);
   if (sums)
     hipLaunchKernelGGL(norm_sums_kernel, dim3((unsigned)((a.D + 63) / 64), 3), dim3(1024), 0, stream, a, parts);
   return hipGetLastError();
 }
 
 template <typename XT, typename HT>
-hipError_t fwd_types(const NormArgs& a, hipStream_t stream) {
-  if (a.D <= 512) return fwd_as<XT, HT, 64, 1>(a, stream);
-  if (a.D <= 1024) return fwd_as<XT, HT, 64, 2>(a, stream);
-  if (a.D <= 2048) return fwd_as<XT, HT, 256, 1>(a, stream);
-  if (a.D <= 4096) return fwd_as<XT, HT, 512, 1>(a, stream);
-  if (a.D <= 8192) return fwd_as<XT, HT, 1024, 1>(a, stream);
-  return fwd_as<XT, HT, 1024, 2>(a, stream);
-}
-
-template <typename XT, typename HT>
 hipError_t bwd_types(const NormArgs& a, hipStream_t stream) {
-  if (a.D <= 512) return bwd_as<XT, HT, 64, 1>(a, stream);
-  if (a.D <= 1024) return bwd_as<XT, HT, 64, 2>(a, stream);
-  if (a.D <= 2048) return bwd_as<XT, HT, 256, 1>(a, stream);
-  if (a.D <= 4096) return bwd_as<XT, HT, 512, 1>(a, stream);
-  if (a.D <= 8192) return bwd_as<XT, HT, 1024, 1>(a, stream);
-  return bwd_as<XT, HT, 1024, 2>(a, stream);
+  const bool al = a.D % 8 == 0;
+  if (a.D <= 8192) return al ? bwd_as<XT, HT, 1, true>(a, stream) : bwd_as<XT, HT, 1, false>(a, stream);
+  return al ? bwd_as<XT, HT, 2, true>(a, stream) : bwd_as<XT, HT, 2, false>(a, stream);
 }
 
 }  // namespace
 
-// One partial row per row group of a workgroup; a multiple of the row groups
-// per workgroup, every one of which writes its partials (zeros past the end).
 int64_t norm_bwd_parts(int64_t T, int64_t D) {
-  const int tpr = row_threads(D), rows = wg_threads(tpr) / tpr;
-  int64_t groups = (T + rows - 1) / rows;
-  if (groups > kBwdGroups) groups = kBwdGroups;
-  return groups * rows;
+  const Walk w = walk_of(T, D);
+  const int64_t groups = (T + w.rows - 1) / w.rows;
+  return groups < w.groups ? groups : w.groups;
 }
 
 hipError_t launch_norm_fwd(const NormArgs& a, bool x_f32, bool h_f32, hipStream_t stream) {

@@ -17,14 +17,25 @@ qlora_linear_fwd / qlora_linear_bwd on bf16 operands. The glue around them
 part of the layer, and runs as plain fp32 torch ops. Only the adapters and
 the block input receive gradients. With checkpoint=True the forward keeps
 only the block input for the backward and runs again inside it.
+
+With `fused` the glue runs on the library's kernels instead: the norms and
+the residual update as qlora_norm_residual_fwd / _bwd, 16-bit between the
+linears. That form also takes what the plain one lacks: rotary positions
+(qlora_rope), norms behind the branches, gates and a residual scale
+    h = x + c * t1 * post1(L_o(...)),  y = h + c * t2 * post2(L_down(...)),
+gradients for the norm gains and gates that require them, and decoding from
+a paged key-value cache (prefill, decode). The attention core and SiLU stay
+fp32 torch ops.
 """
 
 import math
 
 import torch
 import torch.utils.checkpoint
+from torch.autograd.function import once_differentiable
 
 from . import binding as B
+from . import decoder as D
 
 LINEARS = ("q", "k", "v", "o", "gate", "up", "down")
 EPS = 1e-6
@@ -73,8 +84,108 @@ class QLoraLinear:
         Y = _QLoraLinearFn.apply(X, self.A, self.B, self)
         return Y.float().reshape(*lead, self.out_features)
 
+    def bf16(self, X):
+        """X: bf16 [tokens, in] -> bf16 [tokens, out]."""
+        return _QLoraLinearFn.apply(X.contiguous(), self.A, self.B, self)
+
     def storage_bytes(self):
         return sum(self.qw.sizes.values())
+
+
+class _NormResidualFn(torch.autograd.Function):
+    """qlora_norm_residual_fwd with its backward."""
+
+    @staticmethod
+    def forward(ctx, x, h, w_pre, w_post, gate, alpha, eps, n_dtype):
+        xo, n = D.qlora_norm_residual_fwd(x, h, w_pre, w_post, gate, alpha, eps, n_dtype if h is None else None)
+        need_h = w_post is not None or ctx.needs_input_grad[4]
+        ctx.save_for_backward(xo if w_pre is not None else None, h if need_h else None, w_pre, w_post, gate)
+        ctx.args = (None if h is None else h.dtype, alpha, eps)
+        ctx.set_materialize_grads(False)
+        return xo, n
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dxo, dn):
+        if dxo is None and dn is None:
+            return (None,) * 8
+        xo, h, w_pre, w_post, gate = ctx.saved_tensors
+        ht, alpha, eps = ctx.args
+        dxo = None if dxo is None else dxo.contiguous()
+        dn = None if dn is None else dn.contiguous()
+        need = ctx.needs_input_grad
+        gains = [name for i, name in ((2, "w_pre"), (3, "w_post"), (4, "gate")) if need[i]]
+        if xo is None:
+            xo = dxo      # no norm of the stream: its values do not matter
+        dh = torch.empty(xo.shape, dtype=ht, device=xo.device) if ht is not None and need[1] else None
+        gr = D.qlora_norm_residual_bwd(dxo, dn, xo, h, w_pre if dn is not None else None, w_post, gate, alpha, eps,
+                                       need_dh=dh is not None, need_gains=gains, dh=dh)
+        return gr.dx, gr.dh, gr.dw_pre, gr.dw_post, gr.dgate, None, None, None
+
+
+def norm_residual(x, h=None, w_pre=None, w_post=None, gate=None, alpha=1.0, eps=EPS, n_dtype=torch.bfloat16):
+    """Differentiable qlora_norm_residual_fwd: (xo, n).  Without h, xo is x and n
+    has n_dtype; without w_pre, n is None."""
+    return _NormResidualFn.apply(x.contiguous(), None if h is None else h.contiguous(), w_pre, w_post, gate, alpha, eps,
+                                 n_dtype)
+
+
+class _RopeFn(torch.autograd.Function):
+    """qlora_rope; the backward turns the other way."""
+
+    @staticmethod
+    def forward(ctx, q, k, table, positions):
+        ctx.args = (table, positions)
+        return D.qlora_rope(q, k, table, positions)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk):
+        table, positions = ctx.args
+        dq, dk = D.qlora_rope(dq.contiguous(), dk.contiguous(), table, positions, inverse=True)
+        return dq, dk, None, None
+
+
+def rope(q, k, table, positions):
+    """Differentiable qlora_rope of q and k [T, heads, head_dim]."""
+    return _RopeFn.apply(q, k, table, positions)
+
+
+class PagedCache:
+    """The paged key-value cache of one block for up to `max_seqs` sequences of
+    up to `max_len` tokens: bfloat16 pages [num_pages, heads, page_size,
+    head_dim] of keys and values, the block table, and the pages not in use.
+    The lengths are known to the host too, so running out of room raises
+    before anything is enqueued."""
+
+    def __init__(self, num_pages, page_size, heads, head_dim, max_seqs, max_len, device=None):
+        dev = device if device is not None else torch.device("cuda", torch.cuda.current_device())
+        shape = (num_pages, heads, page_size, head_dim)
+        self.k = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
+        self.v = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
+        self.page_size, self.max_len = int(page_size), int(max_len)
+        self.free = torch.arange(num_pages, dtype=torch.int32, device=dev)
+        self.table = torch.full((max_seqs, -(-self.max_len // page_size)), -1, dtype=torch.int32, device=dev)
+        self.lens = torch.zeros(max_seqs, dtype=torch.int32, device=dev)
+        self.host_lens = [0] * max_seqs
+        self.used = 0
+
+    def add(self, new_lens):
+        """Room for new_lens[s] more tokens of each sequence: the PagedPlan of
+        their rows, in order of the sequences."""
+        if len(new_lens) != len(self.host_lens) or any(n < 0 for n in new_lens):
+            raise ValueError(f"new_lens must be {len(self.host_lens)} counts")
+        total = [c + n for c, n in zip(self.host_lens, new_lens)]
+        if max(total) > self.max_len:
+            raise ValueError(f"a sequence would pass max_len = {self.max_len} tokens")
+        p = self.page_size
+        need = sum(-(-t // p) - -(-c // p) for t, c in zip(total, self.host_lens))
+        if self.used + need > self.free.numel():
+            raise ValueError(f"{need} pages needed, {self.free.numel() - self.used} left")
+        new = torch.tensor(new_lens, dtype=torch.int32).to(self.lens.device)
+        plan = D.qlora_paged_plan(self.lens, new, self.free[self.used:], self.table, p, sum(new_lens))
+        self.lens, self.host_lens, self.used = plan.total_lens, total, self.used + need
+        return plan
 
 
 def rms_norm(z, g):
@@ -100,13 +211,23 @@ def causal_attention(q, k, v, heads):
 class QLoraBlock:
     """The decoder block above.  `W`, `A`, `Bm`: dicts by linear name of fp32
     device tensors (W [out, in]); g1, g2: fp32 [hidden] norm gains; s =
-    alpha / r."""
+    alpha / r.  The rest belongs to the fused form: rope a decoder.RopeTable,
+    post1 / post2 and gate1 / gate2 fp32 [hidden] gains and gates of the two
+    branches, residual_scale c; giving any of them implies `fused`."""
 
-    def __init__(self, W, A, Bm, g1, g2, s, heads):
+    def __init__(self, W, A, Bm, g1, g2, s, heads, rope=None, post1=None, post2=None, gate1=None, gate2=None,
+                 residual_scale=1.0, fused=None):
         self.lin = {n: QLoraLinear(W[n], A[n], Bm[n], s) for n in LINEARS}
         self.g1, self.g2 = g1.float(), g2.float()
         self.heads = int(heads)
         self.hidden = W["q"].shape[1]
+        self.rope = rope
+        self.post1, self.post2, self.gate1, self.gate2 = post1, post2, gate1, gate2
+        self.residual_scale = float(residual_scale)
+        extras = self.residual_scale != 1.0 or any(v is not None for v in (rope, post1, post2, gate1, gate2))
+        self.fused = extras if fused is None else bool(fused)
+        if extras and not self.fused:
+            raise ValueError("rope, post norms, gates and a residual scale need the fused form")
 
     def parameters(self):
         """The trainable tensors: every adapter's A and B."""
@@ -123,10 +244,78 @@ class QLoraBlock:
         n2 = rms_norm(h, self.g2)
         return h + L["down"](torch.nn.functional.silu(L["gate"](n2)) * L["up"](n2))
 
+    def _fused(self, x, attend):
+        """The fused form on [..., hidden]: `attend` maps the linears' bf16 q, k,
+        v [tokens, heads, head_dim] to the attention's bf16 [tokens, hidden]."""
+        L, c, T = self.lin, self.residual_scale, x.numel() // self.hidden
+        x, n1 = norm_residual(x, None, self.g1)
+        n1 = n1.reshape(T, self.hidden)
+        q, k, v = (L[n].bf16(n1).view(T, self.heads, -1) for n in ("q", "k", "v"))
+        o = L["o"].bf16(attend(q, k, v)).view(x.shape)
+        h, n2 = norm_residual(x, o, self.g2, self.post1, self.gate1, c)
+        n2 = n2.reshape(T, self.hidden)
+        m = torch.nn.functional.silu(L["gate"].bf16(n2).float()) * L["up"].bf16(n2).float()
+        d = L["down"].bf16(m.to(torch.bfloat16)).view(x.shape)
+        return norm_residual(h, d, None, self.post2, self.gate2, c)[0]
+
+    def _fused_forward(self, x):
+        b, t, _ = x.shape
+
+        def attend(q, k, v):
+            if self.rope is not None:
+                pos = torch.arange(t, dtype=torch.int32, device=x.device).repeat(b)
+                q, k = rope(q, k, self.rope, pos)
+            q, k, v = (z.float().view(b, t, self.hidden) for z in (q, k, v))
+            return causal_attention(q, k, v, self.heads).reshape(b * t, self.hidden).to(torch.bfloat16)
+
+        return self._fused(x, attend)
+
+    def cache(self, num_pages, page_size, max_seqs, max_len):
+        """A PagedCache for this block."""
+        return PagedCache(num_pages, page_size, self.heads, self.hidden // self.heads, max_seqs, max_len,
+                          self.lin["q"].A.device)
+
+    @torch.no_grad()
+    def prefill(self, x, cache):
+        """The first tokens x [batch, seq, hidden] of the cache's sequences 0 ..
+        batch - 1: the block's output, with their keys and values stored."""
+        if not self.fused or x.dim() != 3 or x.shape[0] > len(cache.host_lens) or any(cache.host_lens):
+            raise ValueError("prefill needs a fused block, x [batch, seq, hidden] and an empty cache of as many sequences")
+        b, t, _ = x.shape
+        plan = cache.add([t if s < b else 0 for s in range(len(cache.host_lens))])
+
+        def attend(q, k, v):
+            if self.rope is not None:
+                q, k = D.qlora_rope(q, k, self.rope, plan.positions)
+            D.qlora_rope_cache_write(None, k, v, None, None, plan.slots, cache.k, cache.v)
+            q, k, v = (z.float().view(b, t, self.hidden) for z in (q, k, v))
+            return causal_attention(q, k, v, self.heads).reshape(b * t, self.hidden).to(torch.bfloat16)
+
+        return self._fused(x, attend)
+
+    @torch.no_grad()
+    def decode(self, x, cache):
+        """One more token x [sequences, hidden] for every sequence of the cache:
+        the block's output."""
+        S = len(cache.host_lens)
+        if not self.fused or tuple(x.shape) != (S, self.hidden):
+            raise ValueError(f"decode needs a fused block and x [{S}, {self.hidden}]")
+        plan = cache.add([1] * S)
+
+        def attend(q, k, v):
+            q = D.qlora_rope_cache_write(q, k, v, self.rope, plan.positions, plan.slots, cache.k, cache.v)
+            return D.qlora_paged_attention(q, cache.k, cache.v, cache.table, cache.lens).view(S, self.hidden)
+
+        return self._fused(x, attend)
+
     def __call__(self, x, checkpoint=False):
         """x: fp32 [batch, seq, hidden] -> y (same shape)."""
         if x.shape[-1] != self.hidden:
             raise ValueError(f"x must end in the hidden size {self.hidden}")
+        if self.fused:
+            if checkpoint:
+                return torch.utils.checkpoint.checkpoint(self._fused_forward, x, use_reentrant=False)
+            return self._fused_forward(x)
         if checkpoint:
             return torch.utils.checkpoint.checkpoint(self._forward, x, use_reentrant=False)
         return self._forward(x)

@@ -185,7 +185,8 @@ def qlora_norm_residual_bwd(dxo, dn, xo, h=None, w_pre=None, w_post=None, gate=N
     gradients of its outputs, xo the stream it returned, h its branch (needed
     for w_post and the gradient of the gate).  Returns NormGrads: dx, dh (None
     without need_dh) and, with need_gains, the float32 gradients of the gains
-    and the gate that the forward had."""
+    and the gate that the forward had; need_gains may also name the wanted ones
+    of "w_pre", "w_post" and "gate"."""
     shape, xt = xo.shape, xo.dtype
     D = shape[-1]
     T = xo.numel() // D if D else 0
@@ -210,10 +211,11 @@ def qlora_norm_residual_bwd(dxo, dn, xo, h=None, w_pre=None, w_post=None, gate=N
     dw_pre = dw_post = dgate = ws = None
     nws = 0
     if need_gains:
+        wanted = ("w_pre", "w_post", "gate") if need_gains is True else need_gains
         new = lambda: torch.empty(D, dtype=torch.float32, device=xo.device)  # noqa: E731
-        dw_pre = new() if dn is not None else None
-        dw_post = new() if w_post is not None else None
-        dgate = new() if gate is not None else None
+        dw_pre = new() if dn is not None and "w_pre" in wanted else None
+        dw_post = new() if w_post is not None and "w_post" in wanted else None
+        dgate = new() if gate is not None and "gate" in wanted else None
         nws = _norm_bwd_workspace(T, D, _DTYPES[xt], _DTYPES[hd])
         ws = torch.empty(nws, dtype=torch.uint8, device=xo.device)
     _call("qlora_norm_residual_bwd", _ptr(dxo), xo.data_ptr(), _DTYPES[xt], _ptr(dn), _ptr(h), _DTYPES[hd], T, D,

@@ -9,13 +9,18 @@ fp64 (oracle side).  Test infrastructure only; see the package docstring.
   paged_attention                       attention of one token over a paged
       cache
   paged_plan                            pages, slots and positions of a batch
+  block                                 the decoder block of oracle/block.py with
+      rotary positions, norms behind the branches, gates and a residual scale
 
-numpy only; nothing is shared with the HIP path.
+numpy (torch's fp64 autograd for the block); nothing is shared with the HIP path.
 """
 
 import math
 
 import numpy as np
+import torch
+
+from . import block as oblock
 
 
 def _f(a):
@@ -157,3 +162,51 @@ def paged_plan(cached, new, free, table, page, tokens):
     pad = tokens - len(slots)
     return table, np.array(total, np.int64), np.array(starts), np.array(slots + [-1] * pad), \
         np.array(positions + [0] * pad), used
+
+
+# --------------------------------------------------------------------- block
+
+def _rope_torch(z, freq, mscale, interleaved):
+    """z [batch, seq, heads, d] at positions 0 .. seq - 1."""
+    r = 2 * len(freq)
+    t = torch.arange(z.shape[1], dtype=torch.float64)[:, None, None] * torch.tensor(freq)
+    c, s = mscale * torch.cos(t), mscale * torch.sin(t)
+    p = z[..., :r]
+    x, y = (p[..., 0::2], p[..., 1::2]) if interleaved else (p[..., :r // 2], p[..., r // 2:])
+    x, y = x * c - y * s, x * s + y * c
+    p = torch.stack((x, y), -1).flatten(-2) if interleaved else torch.cat((x, y), -1)
+    return torch.cat((p, z[..., r:]), -1)
+
+
+def block(x, W, A, B, s, heads, gains, rope=None, scale=1.0, dy=None):
+    """The block of oracle/block.py with h = x + scale * gate1 * post1(L_o(..))
+    and likewise after L_down.  gains: dict with g1, g2 and any of post1, post2,
+    gate1, gate2; rope: (frequencies, factor, interleaved) or None.  Returns y,
+    or with dy (y, dx, dA, dB, dgains) as numpy arrays."""
+    t = lambda a, g=False: torch.tensor(_f(a), requires_grad=g)  # noqa: E731
+    xt, gt = t(x, True), {n: t(v, True) for n, v in gains.items()}
+    At, Bt, Wt = {n: t(v, True) for n, v in A.items()}, {n: t(v, True) for n, v in B.items()}, {n: t(W[n]) for n in W}
+
+    def L(n, X):
+        return oblock.qlora_linear(X, Wt[n], At[n], Bt[n], s)
+
+    def step(x, u, i):
+        if f"post{i}" in gt:
+            u = oblock.rms_norm(u, gt[f"post{i}"])
+        if f"gate{i}" in gt:
+            u = u * gt[f"gate{i}"]
+        return x + scale * u
+
+    b, n, hid = xt.shape
+    n1 = oblock.rms_norm(xt, gt["g1"])
+    q, k = L("q", n1), L("k", n1)
+    if rope is not None:
+        q, k = (_rope_torch(z.view(b, n, heads, -1), *rope).reshape(b, n, hid) for z in (q, k))
+    h = step(xt, L("o", oblock.causal_attention(q, k, L("v", n1), heads)), 1)
+    n2 = oblock.rms_norm(h, gt["g2"])
+    y = step(h, L("down", torch.nn.functional.silu(L("gate", n2)) * L("up", n2)), 2)
+    if dy is None:
+        return y.detach().numpy()
+    (y * t(dy)).sum().backward()
+    num = lambda d: {k: v.grad.numpy() for k, v in d.items()}  # noqa: E731
+    return y.detach().numpy(), xt.grad.numpy(), num(At), num(Bt), num(gt)

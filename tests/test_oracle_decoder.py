@@ -139,3 +139,41 @@ def test_paged_plan_invariants():
             assert slots[r] == t2[s, pos[r] // page] * page + pos[r] % page
     _, _, _, slots, _, need = od.paged_plan([0], [10], [7], [[-1, -1]], 4, 10)   # the free list runs out
     assert need == 3 and slots.tolist() == [28, 29, 30, 31] + [-1] * 6
+
+
+def test_block_reduces_to_the_plain_block():
+    """Without the additions it is oracle/block.py's; gates of one, a scale of
+    one and a turn of nothing change nothing; with them, finite differences."""
+    from oracle import block as oblock
+    rng = np.random.default_rng(6)
+    hid, mlp, heads, r, b, n = 16, 24, 2, 3, 2, 5
+    sh = oblock.shapes(hid, mlp)
+    W = {k: 0.3 * _rand(rng, *v) for k, v in sh.items()}
+    A = {k: 0.3 * _rand(rng, v[1], r) for k, v in sh.items()}
+    B = {k: 0.3 * _rand(rng, r, v[0]) for k, v in sh.items()}
+    g = {"g1": 1 + 0.1 * _rand(rng, hid), "g2": 1 + 0.1 * _rand(rng, hid)}
+    x, dy = _rand(rng, b, n, hid), _rand(rng, b, n, hid)
+    y0, dx0, dA0, dB0 = oblock.forward_backward(x, W, A, B, g["g1"], g["g2"], 0.5, heads, dy)
+    y, dx, dA, dB, _ = od.block(x, W, A, B, 0.5, heads, g, dy=dy)
+    assert np.allclose(y, y0) and np.allclose(dx, dx0) and all(np.allclose(dA[k], dA0[k]) for k in dA)
+    one = np.ones(hid)
+    assert np.allclose(od.block(x, W, A, B, 0.5, heads, dict(g, gate1=one, gate2=one),
+                                rope=(np.zeros(4), 1.0, False)), y0)
+    full = dict(g, post1=1 + 0.1 * _rand(rng, hid), post2=1 + 0.1 * _rand(rng, hid), gate1=_rand(rng, hid),
+                gate2=_rand(rng, hid))
+    f = od.rope_frequencies(8)[0]
+    for inter in (False, True):
+        args = dict(rope=(f, 1.1, inter), scale=0.7)
+        y, dx, _, dB, dg = od.block(x, W, A, B, 0.5, heads, full, dy=dy, **args)
+        v = _rand(rng, b, n, hid)
+        hi, lo = (od.block(x + e * v, W, A, B, 0.5, heads, full, **args) for e in (1e-5, -1e-5))
+        assert np.isclose(((hi - lo) * dy).sum() / 2e-5, (dx * v).sum(), rtol=1e-5)
+        for name in full:
+            v = _rand(rng, hid)
+            hi, lo = (od.block(x, W, A, B, 0.5, heads, dict(full, **{name: full[name] + e * v}), **args)
+                      for e in (1e-5, -1e-5))
+            assert np.isclose(((hi - lo) * dy).sum() / 2e-5, (dg[name] * v).sum(), rtol=1e-5), name
+        # the rotation used here is the other one's
+        z = _rand(rng, 1, n, 2, 12)
+        assert np.allclose(od._rope_torch(torch.tensor(z), f, 1.1, inter).numpy()[0],
+                           od.rope(z[0], np.arange(n), f, 1.1, inter))

@@ -153,24 +153,28 @@ hipError_t launch_paged_plan(const PlanArgs& a, hipStream_t stream) {
 //     tokens in the order in which the scores' lanes hold them, so P goes from
 //     the exponentials into the operand without leaving its lane; V^T comes
 //     from a [token][d] tile in LDS by transposed reads.
-// The sums of the weights are fp32 sums of the weights before they are rounded
-// to bfloat16 for the product.  The rows of V behind the length are put as
+// A weight enters the product as two bfloat16 parts, rounded and remainder, so
+// it carries 16 bits (one part alone left the outputs 2.2e-3 rel-L2 from the
+// exact ones, two 1.7e-3, the rounding of the output itself; the second product
+// hides under the loads: 280.3 and 280.6 us at 8 sequences of 32768 to 65536, 64
+// on 8 heads).  The sums of the weights are fp32.  The rows of V behind the length are put as
 // zeros into LDS (0 times what lies there would not be 0 for an infinity), the
 // scores there are replaced, not added to.
 
 namespace {
 
-constexpr int kTile = 32;      // tokens per wave and step
+constexpr int kTile = 32;     // tokens per wave and step
+constexpr int kMinTiles = 2;  // per wave, before a sequence is cut further
 
 // How a sequence of n tokens is cut: `parts` ranges of `per` tiles (the last
-// may be shorter).  No range is shorter than one tile per wave.
+// may be shorter).
 struct Cut {
   int64_t tiles, per, parts;
 };
 __device__ __forceinline__ Cut cut_of(int64_t n, int splits, int waves) {
   Cut c;
   c.tiles = (n + kTile - 1) / kTile;
-  int64_t most = (c.tiles + waves - 1) / waves;
+  int64_t most = (c.tiles + waves * kMinTiles - 1) / (waves * kMinTiles);
   if (most > splits) most = splits;
   if (most < 1) most = 1;
   c.per = (c.tiles + most - 1) / most;
@@ -324,13 +328,19 @@ __global__ __launch_bounds__(64 * W) void paged_attention_kernel(AttnArgs a, int
     }
     const uint4 pw = make_uint4(pack_bf2(p[0], p[1]), pack_bf2(p[2], p[3]), pack_bf2(p[4], p[5]), pack_bf2(p[6], p[7]));
     const bf16x8 pb = __builtin_bit_cast(bf16x8, pw);
+    const uint32_t hi[4] = {pw.x, pw.y, pw.z, pw.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] -= __uint_as_float((j & 1) ? hi[j >> 1] & 0xFFFF0000u : hi[j >> 1] << 16);
+    const uint4 rw = make_uint4(pack_bf2(p[0], p[1]), pack_bf2(p[2], p[3]), pack_bf2(p[4], p[5]), pack_bf2(p[6], p[7]));
+    const bf16x8 rb = __builtin_bit_cast(bf16x8, rw);
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int i = 0; i < DP / 16; ++i) {
       const __bf16* src = vt + (4 * g + (col >> 2)) * PITCH + 16 * i + 4 * (col & 3);
-      const short4_t lo = ds_read_tr16(src), hi = ds_read_tr16(src + 16 * PITCH);
-      const short8_t v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      const short4_t v0 = ds_read_tr16(src), v1 = ds_read_tr16(src + 16 * PITCH);
+      const short8_t v = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
       acc[i] = mfma16(__builtin_bit_cast(bf16x8, v), pb, acc[i]);
+      acc[i] = mfma16(__builtin_bit_cast(bf16x8, v), rb, acc[i]);
     }
   }
 
@@ -429,24 +439,28 @@ void attention_waves(const AttnArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// Eight waves per workgroup where the table can hold sequences of more than
-// 1024 tokens, else four: short sequences leave the waves behind the last tile
-// idle (64 sequences of 1 to 512 tokens, 32 heads of 128: 53 us with four, 63
-// with eight), long ones read a little faster with fewer, longer streams (64
-// of 1 to 2048: 206 and 194 us; 8 of 32768 to 65536, 8 kv heads: 293 and 283).
-// Heads of more than 128 keep four: eight waves' registers and V tiles would
-// leave a CU nothing else.
-static int waves_for(int head_dim, int64_t max_len) { return max_len > 1024 && head_dim <= 128 ? 8 : 4; }
+// Eight waves per workgroup for large calls (by what the table can hold: 128
+// tiles per CU), else four: with fewer, longer streams large calls read a little
+// faster (64 sequences of 1 to 2048, 32 heads: 197 us with four, 188 with eight;
+// 8 of 32768 to 65536, 8 kv heads: 284 and 280), in smaller ones the waves run
+// out of tiles (10 of 5165, 8 kv heads: 47 us and 53; 4 of 2048, 32 heads: 31
+// and 38).  Heads of more than 128 keep four: eight waves' registers and V tiles
+// would leave a CU nothing else.
+static int waves_for(int64_t groups, int head_dim, int64_t max_len) {
+  return groups * ((max_len + kTile - 1) / kTile) >= 128 * 256 && head_dim <= 128 ? 8 : 4;
+}
+static int64_t groups_of(int64_t S, int q_heads, int kv_heads) {
+  return S * kv_heads * ((q_heads / kv_heads + 15) / 16);
+}
 
 // No split up to 512 tokens, where one launch takes less than two (1 sequence
-// of 512, 32 heads: 9.5 us against 14); else enough workgroups for four per
-// CU, as far as the length gives each wave a tile.
+// of 512, 32 heads: 9.5 us against 14); else enough workgroups for four per CU,
+// as far as the length gives each wave its tiles.
 int paged_splits(int64_t S, int q_heads, int kv_heads, int head_dim, int64_t max_len) {
   if (S == 0 || max_len <= 512) return 1;
-  const int waves = waves_for(head_dim, max_len);
-  const int64_t wgs = S * kv_heads * ((q_heads / kv_heads + 15) / 16);
-  int64_t n = (4 * 256 * (8 / waves) + wgs - 1) / wgs;
-  const int64_t most = (max_len + waves * kTile - 1) / (waves * kTile);
+  const int64_t groups = groups_of(S, q_heads, kv_heads), waves = waves_for(groups, head_dim, max_len);
+  int64_t n = (4 * 256 + groups - 1) / groups;
+  const int64_t least = waves * kMinTiles * kTile, most = (max_len + least - 1) / least;
   if (n > most) n = most;
   if (n > kMaxSplits) n = kMaxSplits;
   return n < 1 ? 1 : (int)n;
@@ -454,7 +468,7 @@ int paged_splits(int64_t S, int q_heads, int kv_heads, int head_dim, int64_t max
 
 hipError_t launch_paged_attention(const AttnArgs& args, hipStream_t stream) {
   AttnArgs a = args;
-  a.waves = waves_for(a.head_dim, a.table_cols << a.page_shift);
+  a.waves = waves_for(groups_of(a.S, a.q_heads, a.kv_heads), a.head_dim, a.table_cols << a.page_shift);
   if (a.head_dim <= 64) attention_waves<64>(a, stream);
   else if (a.head_dim <= 96) attention_waves<96>(a, stream);
   else if (a.head_dim <= 128) attention_waves<128>(a, stream);

@@ -64,10 +64,11 @@ int check_rows(int64_t T, int64_t D, float eps, const char* fn) {
 
 int64_t norm_ws(int64_t T, int64_t D) { return T == 0 ? 0 : 3 * norm_bwd_parts(T, D) * D * 4; }
 
-// Sizes and strides of a rotary call; `k_kind` names the keys' rows.
+// Sizes and strides of a rotary call.
 int check_rope(int64_t q_stride, int32_t q_heads, int64_t qo_stride, int64_t k_stride, int32_t kv_heads, int64_t T,
                int32_t head_dim, int32_t rot_dim, int32_t interleaved, int32_t inverse, const char* fn) {
-  if (T < 0 || T > kMaxRows) return fail(QLORA_ERR_INVALID_ARG, "%s: T must be in [0, 2^31)", fn);
+  // a workgroup of 256 threads per token at most: a grid holds 2^32 - 1 threads
+  if (T < 0 || T >= (1 << 24)) return fail(QLORA_ERR_INVALID_ARG, "%s: T must be in [0, 2^24)", fn);
   if (head_dim < 1 || head_dim > 1024) return fail(QLORA_ERR_INVALID_ARG, "%s: head_dim must be in [1, 1024]", fn);
   if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 2)
     return fail(QLORA_ERR_INVALID_ARG, "%s: rot_dim must be even and in [0, head_dim]", fn);
@@ -289,6 +290,8 @@ int qlora_paged_plan(const int32_t* cached_lens, const int32_t* new_lens, int64_
     return st;
   if (S && table_cols && (st = check_ptr(table, "table", fn, 4))) return st;
   if (n_free && (st = check_ptr(free_pages, "free_pages", fn, 4))) return st;
+  if (S && (total_lens == cached_lens || total_lens == new_lens))
+    return fail(QLORA_ERR_INVALID_ARG, "%s: total_lens must not be cached_lens or new_lens", fn);
   if (T && ((st = check_ptr(slots, "slots", fn, 4)) || (st = check_ptr(positions, "positions", fn, 4)))) return st;
   PlanArgs a = {};
   a.cached = cached_lens, a.fresh = new_lens, a.free_pages = free_pages, a.table = table;

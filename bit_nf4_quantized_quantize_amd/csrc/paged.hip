@@ -25,9 +25,17 @@ __device__ __forceinline__ int pages_of(int32_t tokens, const Div& page) {
 }
 // A sequence's length from one of the caller's: not negative.
 __device__ __forceinline__ int32_t length_of(const int32_t* v, int64_t s) { return v[s] < 0 ? 0 : v[s]; }
-__device__ __forceinline__ int32_t clamped_sum(int32_t c, int32_t n) {
-  const int64_t v = (int64_t)c + n;
+// a + b of numbers that are not negative, at most 2^31 - 1: sums of lengths that
+// make no sense stay in order, so nothing is searched or addressed out of
+// bounds by them.
+__device__ __forceinline__ int32_t add_sat(int32_t a, int32_t b) {
+  const uint32_t v = (uint32_t)a + (uint32_t)b;
   return v > INT32_MAX ? INT32_MAX : (int32_t)v;
+}
+// Pages of a sequence of `tokens` that the table has room for.
+__device__ __forceinline__ int32_t held(int32_t tokens, const Div& page, int64_t cols) {
+  const int32_t p = pages_of(tokens, page);
+  return p < cols ? p : (int32_t)cols;
 }
 
 // The largest s < n with v[s] <= i (v[0] <= i).
@@ -52,29 +60,30 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a, in
 #pragma unroll 4
   for (int s = s0; s < s1; ++s) {
     const int32_t c = length_of(a.cached, s), n = length_of(a.fresh, s);
-    const int32_t p = pages_of(clamped_sum(c, n), page) - pages_of(c, page);
+    const int32_t p = held(add_sat(c, n), page, a.table_cols) - held(c, page, a.table_cols);
     starts[s] = n, first[s] = p;
-    nt += n, np += p;
+    nt = add_sat(nt, n), np = add_sat(np, p);
   }
   int32_t vt = nt, vp = np;  // inclusive sums over the wave
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const int32_t ut = __shfl_up(vt, o, 64), up = __shfl_up(vp, o, 64);
-    if (lane >= o) vt += ut, vp += up;
+    if (lane >= o) vt = add_sat(vt, ut), vp = add_sat(vp, up);
   }
   if (lane == 63) wave[0][wv] = vt, wave[1][wv] = vp;
+  vt = __shfl_up(vt, 1, 64), vp = __shfl_up(vp, 1, 64);  // the sums before this thread's
+  if (lane == 0) vt = vp = 0;
   __syncthreads();
   int32_t run_t = 0, run_p = 0;
-  vt -= nt, vp -= np;
 #pragma unroll
   for (int w = 0; w < kPlanThreads / 64; ++w) {
-    if (w < wv) vt += wave[0][w], vp += wave[1][w];
-    run_t += wave[0][w], run_p += wave[1][w];
+    if (w == wv) vt = add_sat(vt, run_t), vp = add_sat(vp, run_p);
+    run_t = add_sat(run_t, wave[0][w]), run_p = add_sat(run_p, wave[1][w]);
   }
   for (int s = s0; s < s1; ++s) {
     const int32_t n = starts[s], p = first[s];
     starts[s] = vt, first[s] = vp;
-    vt += n, vp += p;
+    vt = add_sat(vt, n), vp = add_sat(vp, p);
   }
   if (threadIdx.x == 0) starts[a.S] = run_t, first[a.S] = run_p;
   __syncthreads();
@@ -83,13 +92,13 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a, in
   const int64_t gsz = (int64_t)gridDim.x * kPlanThreads;
   for (int64_t s = gid; s <= a.S; s += gsz) {
     a.starts[s] = starts[s];
-    if (s < a.S) a.total[s] = clamped_sum(length_of(a.cached, s), starts[s + 1] - starts[s]);
+    if (s < a.S) a.total[s] = add_sat(length_of(a.cached, s), length_of(a.fresh, s));
   }
   if (gid == 0) *a.pages_needed = run_p;
   // new table entries, in the order of the free list
   for (int64_t i = gid; i < run_p; i += gsz) {
     const int q = last_at_most(first, a.S, i);
-    const int64_t col = (int64_t)pages_of(length_of(a.cached, q), page) + (i - first[q]);
+    const int64_t col = held(length_of(a.cached, q), page, a.table_cols) + (i - first[q]);
     if (col < a.table_cols) a.table[q * a.table_cols + col] = i < a.n_free ? a.free_pages[i] : -1;
   }
   // token rows: a thread takes `rows` in a row, searches for the first one's
@@ -100,7 +109,7 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a, in
       int32_t slot = -1;
       int64_t pos = 0;
       if (t < run_t) {
-        while (starts[q + 1] <= t) ++q;  // t < starts[S]
+        while (q + 1 < a.S && starts[q + 1] <= t) ++q;
         const int32_t c = length_of(a.cached, q);
         pos = c + (t - starts[q]);
         if (pos <= INT32_MAX) {
@@ -121,7 +130,7 @@ __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a, in
         }
       }
       a.slots[t] = slot;
-      a.positions[t] = (int32_t)pos;
+      a.positions[t] = pos <= INT32_MAX ? (int32_t)pos : INT32_MAX;
     }
   }
 }

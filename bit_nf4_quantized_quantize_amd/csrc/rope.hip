@@ -30,8 +30,8 @@ __device__ __forceinline__ uint16_t from_f<uint16_t>(float v) { return f2bf(v); 
 template <>
 __device__ __forceinline__ float from_f<float>(float v) { return v; }
 
-// EV elements moved at once (16 bytes, or one element where rows do not
-// allow it).
+// EV elements moved at once: 16 bytes, or 8 or one element where rows do not
+// allow it.
 template <typename T, int EV>
 struct alignas(EV * sizeof(T)) Piece {
   T e[EV];
@@ -42,7 +42,7 @@ __device__ __forceinline__ Piece<T, EV> ld(const T* p) { return *reinterpret_cas
 // PAST: 16-byte stores that do not stay in the L2.
 template <typename T, int EV, bool PAST>
 __device__ __forceinline__ void st(T* p, const Piece<T, EV>& v) {
-  if constexpr (PAST && EV > 1) {
+  if constexpr (PAST && EV * sizeof(T) == 16) {
     typedef uint32_t words __attribute__((ext_vector_type(4)));
     __builtin_nontemporal_store(__builtin_bit_cast(words, v), reinterpret_cast<words*>(p));
   } else {
@@ -202,19 +202,26 @@ hipError_t rope_as(const RopeArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+// Whether pieces of ev elements fit: every row, the two halves of the pairs and
+// the rest of the head have to be whole pieces.
+static bool pieces_fit(const RopeArgs& a, int ev) {
+  return a.head_dim % ev == 0 && (a.interleaved ? a.rot_dim : a.rot_dim / 2) % ev == 0 && a.rot_dim % ev == 0 &&
+         a.q_stride % ev == 0 && a.qo_stride % ev == 0 && a.k_stride % ev == 0 && a.ko_stride % ev == 0 &&
+         a.v_stride % ev == 0;
+}
+
+template <typename T>
+static hipError_t rope_of(const RopeArgs& a, hipStream_t stream) {
+  constexpr int WIDE = 16 / sizeof(T);
+  if (pieces_fit(a, WIDE))
+    return a.interleaved ? rope_as<T, WIDE, true>(a, stream) : rope_as<T, WIDE, false>(a, stream);
+  if (pieces_fit(a, WIDE / 2))
+    return a.interleaved ? rope_as<T, WIDE / 2, true>(a, stream) : rope_as<T, WIDE / 2, false>(a, stream);
+  return a.interleaved ? rope_as<T, 1, true>(a, stream) : rope_as<T, 1, false>(a, stream);
+}
+
 hipError_t launch_rope(const RopeArgs& a, bool f32, hipStream_t stream) {
-  // 16-byte pieces need every row, the two halves of the pairs and the rest of
-  // the head to be whole pieces.
-  const int ev = f32 ? 4 : 8;
-  const bool vec = a.head_dim % ev == 0 && (a.interleaved ? a.rot_dim : a.rot_dim / 2) % ev == 0 &&
-                   a.rot_dim % ev == 0 && a.q_stride % ev == 0 && a.qo_stride % ev == 0 && a.k_stride % ev == 0 &&
-                   a.ko_stride % ev == 0 && a.v_stride % ev == 0;
-  if (a.interleaved) {
-    if (f32) return vec ? rope_as<float, 4, true>(a, stream) : rope_as<float, 1, true>(a, stream);
-    return vec ? rope_as<uint16_t, 8, true>(a, stream) : rope_as<uint16_t, 1, true>(a, stream);
-  }
-  if (f32) return vec ? rope_as<float, 4, false>(a, stream) : rope_as<float, 1, false>(a, stream);
-  return vec ? rope_as<uint16_t, 8, false>(a, stream) : rope_as<uint16_t, 1, false>(a, stream);
+  return f32 ? rope_of<float>(a, stream) : rope_of<uint16_t>(a, stream);
 }
 
 }  // namespace qlora

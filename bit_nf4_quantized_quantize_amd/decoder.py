@@ -163,7 +163,7 @@ def qlora_norm_residual_fwd(x, h=None, w_pre=None, w_post=None, gate=None, alpha
     if n is not None:
         _dense(n, "n", shape, (nd,))
     elif w_pre is not None:
-        n = torch.empty_like(x, dtype=nd)
+        n = torch.empty_like(x) if nd == xt else torch.empty_like(x, dtype=nd)
     _call("qlora_norm_residual_fwd", x.data_ptr(), _DTYPES[xt], _ptr(h), _DTYPES[nd], x.numel() // D if D else 0, D,
           _ptr(w_post), _ptr(gate), alpha, _ptr(w_pre), eps, _ptr(xo), _ptr(n), on)
     return (x if xo is None else xo), n
@@ -290,18 +290,22 @@ def qlora_rope(q, k, table, positions, inverse=False, q_out=None, k_out=None, st
     qh = qs = qos = kh = ks = kos = 0
     if q is not None:
         qh, qs = _heads(q, "q", T, d, dt)
-        q_out = torch.empty(q.shape, dtype=dt, device=q.device) if q_out is None else q_out
-        h, qos = _heads(q_out, "q_out", T, d, dt)
-        if h != qh:
-            raise ValueError("q_out must have the heads of q")
+        if q_out is None:
+            q_out, qos = torch.empty(q.shape, dtype=dt, device=q.device), qh * d
+        else:
+            h, qos = _heads(q_out, "q_out", T, d, dt)
+            if h != qh:
+                raise ValueError("q_out must have the heads of q")
     else:
         q_out = None
     if k is not None:
         kh, ks = _heads(k, "k", T, d, dt)
-        k_out = torch.empty(k.shape, dtype=dt, device=k.device) if k_out is None else k_out
-        h, kos = _heads(k_out, "k_out", T, d, dt)
-        if h != kh:
-            raise ValueError("k_out must have the heads of k")
+        if k_out is None:
+            k_out, kos = torch.empty(k.shape, dtype=dt, device=k.device), kh * d
+        else:
+            h, kos = _heads(k_out, "k_out", T, d, dt)
+            if h != kh:
+                raise ValueError("k_out must have the heads of k")
     else:
         k_out = None
     _call("qlora_rope", _ptr(q), qs, qh, _ptr(q_out), qos, _ptr(k), ks, kh, _ptr(k_out), kos, T, d, table.rot_dim,

@@ -127,7 +127,7 @@ int qlora_rope_frequencies(int32_t rot_dim, double base, int32_t scaling, double
  *   interleaved  0: a_i = element i, b_i = element i + rot_dim / 2;
  *             1: a_i = element 2i, b_i = element 2i + 1.
  *   1 <= head_dim <= 1024; rot_dim even, 0 <= rot_dim <= head_dim; strides at
- *   least heads * head_dim.
+ *   least heads * head_dim; T < 2^24.
  * The angle is reduced in fp64, the rotation is fp32, rounded once.
  */
 int qlora_rope(const void* q, int64_t q_stride, int32_t q_heads, void* qo, int64_t qo_stride, const void* k,
@@ -173,16 +173,16 @@ int qlora_rope_cache_write(const void* q, int64_t q_stride, int32_t q_heads, voi
  * s, with cached_lens[s] tokens in the cache, gets new_lens[s] more.
  *
  *   cached_lens, new_lens   int32 [S]; negative values count as 0.  S <=
- *             QLORA_PLAN_MAX_SEQS; all new tokens together, and each cached +
- *             new, must stay below 2^31.
+ *             QLORA_PLAN_MAX_SEQS; sums beyond 2^31 - 1 (all new tokens, or
+ *             cached + new of a sequence) count as 2^31 - 1.
  *   free_pages int32 [n_free]: pages not in use.  The sequences take the pages
  *             they need from its front, in order of s and of position.
  *   table     int32 [S, table_cols]: the block table.  The pages that cached
  *             tokens occupy must be there; the pages taken are written behind
  *             them, every other entry is left as it is.  Where the free list
- *             has run out the entry becomes -1; pages beyond table_cols are
- *             taken but not recorded.
- *   total_lens int32 [S]: cached + new.
+ *             has run out the entry becomes -1; no page is taken that the
+ *             table has no column for.
+ *   total_lens int32 [S]: cached + new; not cached_lens or new_lens themselves.
  *   starts    int32 [S + 1]: the first row of each sequence's new tokens, and
  *             the number of new tokens.
  *   slots, positions  int32 [T]: for the new tokens in order of s, the slot
@@ -190,7 +190,7 @@ int qlora_rope_cache_write(const void* q, int64_t q_stride, int32_t q_heads, voi
  *             behind the last new token get slot -1 and position 0, rows that
  *             T does not hold are left out.
  *   pages_needed  int32 [1]: pages the batch takes; more than n_free means that
- *             some tokens got no slot.
+ *             some tokens got no slot (as do tokens beyond table_cols pages).
  *   page_size >= 1.
  * One launch; integers only, so the result does not depend on the launch.
  */

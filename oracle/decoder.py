@@ -147,13 +147,11 @@ def paged_plan(cached, new, free, table, page, tokens):
         c, n = max(int(c), 0), max(int(n), 0)
         have = -(-c // page)
         mine = {j: int(table[s, j]) for j in range(min(have, cols))}
-        for j in range(have, -(-(c + n) // page)):
-            mine[j] = free[used] if used < len(free) else -1
+        for j in range(have, min(-(-(c + n) // page), cols)):
+            mine[j] = table[s, j] = free[used] if used < len(free) else -1
             used += 1
-            if j < cols:
-                table[s, j] = mine[j]
         for p in range(c, c + n):
-            pg = mine.get(p // page, -1) if p // page < cols else -1
+            pg = mine.get(p // page, -1)
             slots.append(pg * page + p % page if pg >= 0 else -1)
             positions.append(p)
         total.append(c + n)

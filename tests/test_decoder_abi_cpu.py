@@ -90,7 +90,7 @@ def test_rope_refusals():
     f = _caller("qlora_rope", ROPE, dict(q=P, qs=256, qh=4, qo=P + 4096, qos=256, k=P, ks=128, kh=2, ko=P + 4096,
                                          kos=128, T=3, d=64, rot=64, dt=BF16, pos=P, turns=P, m=1.0, inter=0, inv=0,
                                          stream=None))
-    assert f(dt=2) == DT and f(T=-1) == BAD and f(T=2 ** 31) == BAD
+    assert f(dt=2) == DT and f(T=-1) == BAD and f(T=2 ** 24) == BAD
     assert f(d=0) == BAD and f(d=1025) == BAD and f(rot=63) == BAD and f(rot=66) == BAD and f(rot=-2) == BAD
     assert f(qh=-1) == BAD and f(kh=5000) == BAD and f(inter=2) == BAD and f(inv=-1) == BAD
     for k in ("qs", "qos", "ks", "kos"):
@@ -156,7 +156,8 @@ PLAN = ("cached new S page free nfree table cols T total starts slots pos need s
 
 def test_plan_refusals():
     f = _caller("qlora_paged_plan", PLAN, dict(cached=P, new=P, S=3, page=16, free=P, nfree=5, table=P, cols=4, T=9,
-                                               total=P, starts=P, slots=P, pos=P, need=P, stream=None))
+                                               total=P + 64, starts=P, slots=P, pos=P, need=P, stream=None))
+    assert f(total=P) == BAD            # in place of the lengths
     assert f(S=-1) == BAD and f(S=4097) == BAD and f(page=0) == BAD
     for k in ("nfree", "cols", "T"):
         assert f(**{k: -1}) == BAD and f(**{k: 2 ** 31}) == BAD, k

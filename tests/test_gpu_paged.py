@@ -283,7 +283,7 @@ def test_plan_short_of_pages_and_columns(D):
     for spare, cols in ((-5, None), (-10 ** 6, None), (2, 2), (-4, 3)):
         cached, new, free, table = _plan_case(rng, 40, 8, 30, 20, spare, cols)
         p = _check_plan(D, cached, new, free, table, 8, int(new.sum()))
-        if spare < 0:
+        if spare < 0 and cols is None:
             assert int(p.pages_needed) > len(free)
     # a cached page that is missing: its tokens' slots are missing
     _check_plan(D, [5, 3], [2, 4], [9, 8], [[-1, -1], [4, -1]], 8, 6)
@@ -297,6 +297,23 @@ def test_plan_odd_lengths(D):
     z = torch.empty(0, dtype=torch.int32, device="cuda")
     p = D.qlora_paged_plan(z, z, z, torch.empty(0, 3, dtype=torch.int32, device="cuda"), 16, 3)
     assert p.starts.tolist() == [0] and p.slots.tolist() == [-1] * 3 and p.pages_needed.tolist() == [0]
+
+
+def test_plan_lengths_beyond_31_bits(D):
+    """Lengths that make no sense: sums stop at 2^31 - 1, the rows that exist are
+    planned as far as the table goes."""
+    _log("plan lengths beyond 31 bits")
+    big = 2 ** 31 - 1
+    t = _dev([[-7] * 3] * 4)
+    p = D.qlora_paged_plan(_dev([0, 3, big, big]), _dev([big, 7, big, 1]), _dev([5, 6, 7, 8]), t, 16, 40)
+    assert p.starts.tolist() == [0, big, big, big, big] and p.total_lens.tolist() == [big, 10, big, big]
+    assert p.positions.tolist() == list(range(40))
+    assert p.slots.tolist() == [80 + i for i in range(16)] + [96 + i for i in range(16)] + [112 + i for i in range(8)]
+    assert t.tolist() == [[5, 6, 7]] + [[-7] * 3] * 3 and p.pages_needed.tolist() == [3]
+    t = _dev([[4, -7, -7]])
+    p = D.qlora_paged_plan(_dev([big - 2]), _dev([5]), _dev([5, 6]), t, 16, 6)
+    assert p.slots.tolist() == [-1] * 6 and p.positions.tolist() == [big - 2, big - 1, big, big, big, 0]
+    assert t.tolist() == [[4, -7, -7]]
 
 
 def test_plan_graph(D):

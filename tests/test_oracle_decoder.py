@@ -137,8 +137,10 @@ def test_paged_plan_invariants():
         for r in range(starts[s], starts[s + 1]):
             assert pos[r] == cached[s] + r - starts[s]
             assert slots[r] == t2[s, pos[r] // page] * page + pos[r] % page
-    _, _, _, slots, _, need = od.paged_plan([0], [10], [7], [[-1, -1]], 4, 10)   # the free list runs out
+    _, _, _, slots, _, need = od.paged_plan([0], [10], [7], [[-1] * 3], 4, 10)   # the free list runs out
     assert need == 3 and slots.tolist() == [28, 29, 30, 31] + [-1] * 6
+    _, _, _, slots, _, need = od.paged_plan([0], [10], [7, 1, 2], [[-1]], 4, 10)  # the table does
+    assert need == 1 and slots.tolist() == [28, 29, 30, 31] + [-1] * 6
 
 
 def test_block_reduces_to_the_plain_block():

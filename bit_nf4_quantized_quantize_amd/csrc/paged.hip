@@ -391,32 +391,32 @@ __global__ __launch_bounds__(64 * W) void paged_attention_kernel(AttnArgs a, int
 // Joins the parts of a sequence, one workgroup per sequence and head: its
 // threads hold four elements of the head each and take the parts in turns of
 // 1024 / head_dim, then the turns' sums are added in order.
-constexpr int kMaxSplits = 64;
+constexpr int kMaxSplits = 256;
 
 __global__ __launch_bounds__(256) void paged_join_kernel(AttnArgs a) {
-  __shared__ float s_f[kMaxSplits], s_sum;
+  __shared__ float s_f[kMaxSplits], s_m[4], s_l[4];
   __shared__ floatx4 s_o[256];
   const int64_t s = blockIdx.y, row = s * a.q_heads + blockIdx.x;
   const int d = a.head_dim, dq = d / 4, t = threadIdx.x;
   const int parts = (int)cut_of(tokens_of(a, s), a.splits, a.waves).parts;
-  if (t < 64) {
-    float m = -INFINITY, l = 0.0f;
-    if (t < parts) {
-      const float2 v = *reinterpret_cast<const float2*>(a.part_ml + (row * a.splits + t) * 2);
-      m = v.x, l = v.y;
-    }
-    const float mx = wave_max(m), mu = mx == -INFINITY ? 0.0f : mx;
-    const float f = __builtin_amdgcn_exp2f(m - mu);
-    l *= f;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) l += __shfl_xor(l, o, 64);
-    s_f[t] = f;
-    if (t == 0) {
-      s_sum = l == 0.0f ? 0.0f : 1.0f / l;
-      if (a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994530942f;
-    }
+  float m = -INFINITY, l = 0.0f;
+  if (t < parts) {
+    const float2 v = *reinterpret_cast<const float2*>(a.part_ml + (row * a.splits + t) * 2);
+    m = v.x, l = v.y;
   }
+  const float wm = wave_max(m);
+  if ((t & 63) == 0) s_m[t >> 6] = wm;
   __syncthreads();
+  const float mx = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3])), mu = mx == -INFINITY ? 0.0f : mx;
+  const float f = __builtin_amdgcn_exp2f(m - mu);
+  l *= f;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) l += __shfl_xor(l, o, 64);
+  s_f[t] = f;
+  if ((t & 63) == 0) s_l[t >> 6] = l;
+  __syncthreads();
+  const float sum = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]), inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  if (a.lse && t == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994530942f;
   const int turns = 256 / dq, turn = t / dq, c = t - turn * dq;
   floatx4 o = {0, 0, 0, 0};
   if (turn < turns) {
@@ -428,7 +428,7 @@ __global__ __launch_bounds__(256) void paged_join_kernel(AttnArgs a) {
   __syncthreads();
   if (t < dq) {
     for (int k = 1; k < turns; ++k) o += s_o[k * dq + t];
-    o *= s_sum;
+    o *= inv;
     *reinterpret_cast<uint2*>(a.out + row * d + 4 * t) = make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
   }
 }
@@ -464,11 +464,13 @@ static int64_t groups_of(int64_t S, int q_heads, int kv_heads) {
 
 // No split up to 512 tokens, where one launch takes less than two (1 sequence
 // of 512, 32 heads: 9.5 us against 14); else enough workgroups for four per CU,
-// as far as the length gives each wave its tiles.
+// which evens out sequences of different lengths, or two for less than four
+// sequences (1 of 131072, 32 on 8 heads: 105 us with four, 100 with two), as far
+// as the length gives each wave its tiles.
 int paged_splits(int64_t S, int q_heads, int kv_heads, int head_dim, int64_t max_len) {
   if (S == 0 || max_len <= 512) return 1;
   const int64_t groups = groups_of(S, q_heads, kv_heads), waves = waves_for(groups, head_dim, max_len);
-  int64_t n = (4 * 256 + groups - 1) / groups;
+  int64_t n = ((S < 4 ? 2 : 4) * 256 + groups - 1) / groups;
   const int64_t least = waves * kMinTiles * kTile, most = (max_len + least - 1) / least;
   if (n > most) n = most;
   if (n > kMaxSplits) n = kMaxSplits;

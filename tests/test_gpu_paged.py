@@ -85,7 +85,7 @@ SHAPES = [  # S, q heads, kv heads, head_dim, page, columns, lengths
     (2, 34, 2, 64, 128, 3, [384, 200]), (1, 40, 1, 128, 16, 80, [1279]), (4, 7, 7, 256, 16, 20, [320, 3, 64, 65]),
     (2, 64, 8, 128, 64, 33, [2111, 700]), (1, 2, 2, 32, 1024, 2, [1500]), (70, 4, 4, 64, 16, 8, list(range(0, 70))),
     (2, 3, 1, 40, 16, 30, [470, 479]), (1, 8, 8, 192, 16, 20, [300]), (1, 20, 1, 16, 16, 20, [299]),
-    (1, 4, 4, 128, 16, 520, [8311])]
+    (1, 4, 4, 128, 16, 520, [8311]), (1, 2, 1, 64, 64, 1100, [70000]), (2, 3, 1, 128, 16, 2000, [31999, 700])]
 
 
 @pytest.mark.parametrize("S,H,KV,d,page,cols,lengths", SHAPES)

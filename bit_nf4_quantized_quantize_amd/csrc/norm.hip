@@ -4,8 +4,11 @@
 // Both directions are streams over rows of D elements with one or two row
 // means in between, bound by HBM: the forward reads x and h and writes xo and
 // n once, the backward reads dxo, xo, dn and h and writes dx and dh once.  A
-// row is held in the registers of its threads (NV chunks of 8 elements each), so nothing is read twice; 512 elements
-// to a wave (1024 beyond 8192).
+// row is held in the registers of its threads (NV chunks of 8 elements each), so
+// nothing is read twice; 512 elements to a wave (1024 beyond 8192).  Measured:
+// 8192 x 8192 in bfloat16 with every part, forward 108-113 us (4.8-4.95 TB/s,
+// a device copy's rate is 4.9), backward 178 us with the sums (4.5 TB/s); 8191 x
+// 4096 with an fp32 stream, backward 134 us (4.5 TB/s).
 #include "decoder.h"
 #include "device.h"
 

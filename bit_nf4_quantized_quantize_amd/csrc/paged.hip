@@ -196,6 +196,17 @@ __device__ __forceinline__ int64_t tokens_of(const AttnArgs& a, int64_t s) {
   return n < 0 ? 0 : n > cap ? cap : n;
 }
 
+// The pages of the two halves of a tile (-1: none, or behind the length).
+struct Pages {
+  int32_t of[2];
+};
+__device__ __forceinline__ Pages pages_at(const AttnArgs& a, const int32_t* table, int64_t tok, int64_t n) {
+  Pages p;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) p.of[h] = tok + 16 * h < n ? table[(tok + 16 * h) >> a.page_shift] : -1;
+  return p;
+}
+
 // What the lanes of a wave hold of one tile.
 template <int DP>
 struct Tile {
@@ -205,21 +216,18 @@ struct Tile {
 };
 
 template <int DP>
-__device__ __forceinline__ void load_tile(Tile<DP>& t, const AttnArgs& a, const int32_t* table, int64_t tok, int64_t n,
-                                          int kv, int lane) {
+__device__ __forceinline__ void load_tile(Tile<DP>& t, const AttnArgs& a, const Pages& p, int64_t tok, int kv,
+                                          int lane) {
   constexpr int CH = DP / 8;  // 16-byte pieces of a padded row
   const int d = a.head_dim;
   int64_t base[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int64_t first = tok + 16 * h;
-    int32_t page = -1;
-    if (first < n) page = table[first >> a.page_shift];
-    page = __builtin_amdgcn_readfirstlane(page);
+    const int32_t page = __builtin_amdgcn_readfirstlane(p.of[h]);
     t.ok[h] = page >= 0 && page < a.num_pages;
     // without a page the loads go to the cache's first rows and count nothing
-    base[h] = t.ok[h] ? ((((int64_t)page * a.kv_heads + kv) << a.page_shift) + (first & ((1 << a.page_shift) - 1))) * d
-                      : 0;
+    const int64_t first = (tok + 16 * h) & ((1 << a.page_shift) - 1);
+    base[h] = t.ok[h] ? ((((int64_t)page * a.kv_heads + kv) << a.page_shift) + first) * d : 0;
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -280,9 +288,13 @@ __global__ __launch_bounds__(64 * W) void paged_attention_kernel(AttnArgs a, int
   for (int t = 0; t < DP / 16; ++t) acc[t] = (floatx4){0, 0, 0, 0};
   __bf16* vt = reinterpret_cast<__bf16*>(lds + wave * WAVE_BYTES);
 
+  // the loads of the next tile run under the products of this one, and the
+  // look-up of the pages after that, so neither waits for the other
   Tile<DP> t;
   int64_t ti = first + wave;
-  if (ti < last) load_tile<DP>(t, a, table, ti * kTile, n, kv, lane);
+  Pages pages = pages_at(a, table, ti * kTile, n);
+  if (ti < last) load_tile<DP>(t, a, pages, ti * kTile, kv, lane);
+  pages = pages_at(a, table, (ti + W) * kTile, n);
   for (; ti < last; ti += W) {
     const int64_t tok = ti * kTile;
     const bool full = tok + kTile <= n && t.ok[0] && t.ok[1];
@@ -308,7 +320,8 @@ __global__ __launch_bounds__(64 * W) void paged_attention_kernel(AttnArgs a, int
       }
     }
     const bool ok0 = t.ok[0], ok1 = t.ok[1];
-    if (ti + W < last) load_tile<DP>(t, a, table, tok + W * kTile, n, kv, lane);
+    if (ti + W < last) load_tile<DP>(t, a, pages, tok + W * kTile, kv, lane);
+    pages = pages_at(a, table, tok + 2 * W * kTile, n);
     float p[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) p[j] = sc[j >> 2][j & 3] * scale2;

@@ -84,96 +84,111 @@ struct Unit {
 // The heads of a token are cut into units: rotated units (a piece of each
 // half of the pairs, or a piece of whole pairs when interleaved), then pieces
 // of the rest of the head; the values' heads are pieces throughout.
-// blockIdx.y takes a share of a token group's units.  A thread loads UN units
-// before it stores the first.
+struct Cuts {
+  Div units, hu, vu, half;  // per token, per head of q and k, per head of v; pairs of a head
+};
+
+template <typename T, int EV, bool INTER>
+__device__ __forceinline__ void load_unit(Unit<T, EV>& w, const RopeArgs& a, const Cuts& by, int64_t t0, int i) {
+  constexpr int PE = INTER ? (EV > 1 ? EV / 2 : 1) : EV;  // pairs per rotated unit
+  const int half = a.rot_dim / 2, hu = by.hu.d, ru = half / PE, qk = (a.q_heads + a.kv_heads) * hu;
+  const int tk = i / by.units, u = i - tk * (int)by.units.d;
+  const int64_t t = t0 + tk;
+  int32_t slot = 0;
+  if (a.slots) slot = a.slots[t];
+  const bool stored = slot >= 0 && slot < a.num_slots;
+  const T* src;
+  w.trig = w.b = -1;
+  if (u >= qk) {  // values
+    if (!stored) return;
+    const int head = (u - qk) / by.vu;
+    w.a = (u - qk - head * (int)by.vu.d) * EV;
+    src = (const T*)a.v + t * a.v_stride + (int64_t)head * a.head_dim;
+    w.dst = cache_row<T>(a.v_cache, slot, head, a);
+  } else {
+    int head = u / by.hu;
+    const int r = u - head * hu;
+    if (head < a.q_heads) {
+      src = (const T*)a.q + t * a.q_stride + (int64_t)head * a.head_dim;
+      w.dst = (T*)a.qo + t * a.qo_stride + (int64_t)head * a.head_dim;
+    } else {
+      head -= a.q_heads;
+      if (a.slots && !stored) return;
+      src = (const T*)a.k + t * a.k_stride + (int64_t)head * a.head_dim;
+      w.dst = a.slots ? cache_row<T>(a.k_cache, slot, head, a)
+                      : (T*)a.ko + t * a.ko_stride + (int64_t)head * a.head_dim;
+    }
+    if (r < ru) {
+      w.trig = tk * half + r * PE;
+      w.a = INTER ? 2 * r * PE : r * PE;
+      if (!INTER) w.b = half + r * PE;
+      else if (EV == 1) w.b = 2 * r + 1;
+    } else {
+      w.a = a.rot_dim + (r - ru) * EV;
+    }
+  }
+  w.x = ld<T, EV>(src + w.a);
+  if (w.b >= 0) w.y = ld<T, EV>(src + w.b);
+}
+
+template <typename T, int EV, bool INTER, bool PAST>
+__device__ __forceinline__ void store_unit(Unit<T, EV>& w, const float* cs, const float* sn) {
+  if (!w.dst) return;
+  if (w.trig >= 0) {
+    const float* c = cs + w.trig;
+    const float* s = sn + w.trig;
+    if (INTER && EV > 1) {
+#pragma unroll
+      for (int k = 0; k < EV / 2; ++k) {
+        const float x = to_f<T>(w.x.e[2 * k]), y = to_f<T>(w.x.e[2 * k + 1]);
+        w.x.e[2 * k] = from_f<T>(x * c[k] - y * s[k]);
+        w.x.e[2 * k + 1] = from_f<T>(x * s[k] + y * c[k]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < EV; ++k) {
+        const float x = to_f<T>(w.x.e[k]), y = to_f<T>(w.y.e[k]);
+        w.x.e[k] = from_f<T>(x * c[k] - y * s[k]);
+        w.y.e[k] = from_f<T>(x * s[k] + y * c[k]);
+      }
+    }
+  }
+  st<T, EV, PAST>(w.dst + w.a, w.x);
+  if (w.b >= 0) st<T, EV, PAST>(w.dst + w.b, w.y);
+}
+
+// blockIdx.x takes nt tokens, blockIdx.y a share of their units.  A thread
+// loads UN units before it stores the first, the first UN before the cosines
+// are formed.
 template <typename T, int EV, bool INTER, bool PAST, int UN>
-__global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, int nt, Div by_units, Div by_hu, Div by_vu,
-                                                        Div by_half) {
+__global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, int nt, Cuts by) {
   extern __shared__ float trig[];  // [nt][half] cosines, then as many sines
   const int half = a.rot_dim / 2;
   const int64_t t0 = (int64_t)blockIdx.x * nt;
   const int n = (int)(a.T - t0 < nt ? a.T - t0 : nt);
   float* cs = trig;
   float* sn = trig + nt * half;
+  const int total = n * (int)by.units.d, step = gridDim.y * kThreads;
+  int i0 = blockIdx.y * kThreads + threadIdx.x;
+  Unit<T, EV> w[UN];
+  auto load = [&] {
+#pragma unroll
+    for (int j = 0; j < UN; ++j) {
+      w[j].dst = nullptr;
+      if (i0 + j * step < total) load_unit<T, EV, INTER>(w[j], a, by, t0, i0 + j * step);
+    }
+  };
+  load();
   for (int i = threadIdx.x; i < n * half; i += kThreads) {
-    const int tk = i / by_half;
+    const int tk = i / by.half;
     angle(a.positions[t0 + tk], a.turns[i - tk * half], a.mscale, a.inverse, cs + i, sn + i);
   }
   __syncthreads();
-
-  constexpr int PE = INTER ? (EV > 1 ? EV / 2 : 1) : EV;  // pairs per rotated unit
-  const int hu = by_hu.d, ru = half / PE, qk = (a.q_heads + a.kv_heads) * hu, units = by_units.d;
-  const int total = n * units, step = gridDim.y * kThreads;
-  for (int i0 = blockIdx.y * kThreads + threadIdx.x; i0 < total; i0 += UN * step) {
-    Unit<T, EV> w[UN];
+  while (i0 < total) {
 #pragma unroll
-    for (int j = 0; j < UN; ++j) {
-      const int i = i0 + j * step;
-      w[j].dst = nullptr;
-      if (i >= total) continue;
-      const int tk = i / by_units, u = i - tk * units;
-      const int64_t t = t0 + tk;
-      int32_t slot = 0;
-      if (a.slots) slot = a.slots[t];
-      const bool stored = slot >= 0 && slot < a.num_slots;
-      const T* src;
-      w[j].trig = w[j].b = -1;
-      if (u >= qk) {  // values
-        if (!stored) continue;
-        const int head = (u - qk) / by_vu;
-        w[j].a = (u - qk - head * (int)by_vu.d) * EV;
-        src = (const T*)a.v + t * a.v_stride + (int64_t)head * a.head_dim;
-        w[j].dst = cache_row<T>(a.v_cache, slot, head, a);
-      } else {
-        int head = u / by_hu;
-        const int r = u - head * hu;
-        if (head < a.q_heads) {
-          src = (const T*)a.q + t * a.q_stride + (int64_t)head * a.head_dim;
-          w[j].dst = (T*)a.qo + t * a.qo_stride + (int64_t)head * a.head_dim;
-        } else {
-          head -= a.q_heads;
-          if (a.slots && !stored) continue;
-          src = (const T*)a.k + t * a.k_stride + (int64_t)head * a.head_dim;
-          w[j].dst = a.slots ? cache_row<T>(a.k_cache, slot, head, a)
-                             : (T*)a.ko + t * a.ko_stride + (int64_t)head * a.head_dim;
-        }
-        if (r < ru) {
-          w[j].trig = tk * half + r * PE;
-          w[j].a = INTER ? 2 * r * PE : r * PE;
-          if (!INTER) w[j].b = half + r * PE;
-          else if (EV == 1) w[j].b = 2 * r + 1;
-        } else {
-          w[j].a = a.rot_dim + (r - ru) * EV;
-        }
-      }
-      w[j].x = ld<T, EV>(src + w[j].a);
-      if (w[j].b >= 0) w[j].y = ld<T, EV>(src + w[j].b);
-    }
-#pragma unroll
-    for (int j = 0; j < UN; ++j) {
-      if (!w[j].dst) continue;
-      if (w[j].trig >= 0) {
-        const float* c = cs + w[j].trig;
-        const float* s = sn + w[j].trig;
-        if (INTER && EV > 1) {
-#pragma unroll
-          for (int k = 0; k < EV / 2; ++k) {
-            const float x = to_f<T>(w[j].x.e[2 * k]), y = to_f<T>(w[j].x.e[2 * k + 1]);
-            w[j].x.e[2 * k] = from_f<T>(x * c[k] - y * s[k]);
-            w[j].x.e[2 * k + 1] = from_f<T>(x * s[k] + y * c[k]);
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < EV; ++k) {
-            const float x = to_f<T>(w[j].x.e[k]), y = to_f<T>(w[j].y.e[k]);
-            w[j].x.e[k] = from_f<T>(x * c[k] - y * s[k]);
-            w[j].y.e[k] = from_f<T>(x * s[k] + y * c[k]);
-          }
-        }
-      }
-      st<T, EV, PAST>(w[j].dst + w[j].a, w[j].x);
-      if (w[j].b >= 0) st<T, EV, PAST>(w[j].dst + w[j].b, w[j].y);
-    }
+    for (int j = 0; j < UN; ++j) store_unit<T, EV, INTER, PAST>(w[j], cs, sn);
+    i0 += UN * step;
+    load();
   }
 }
 
@@ -195,8 +210,8 @@ hipError_t rope_as(const RopeArgs& a, hipStream_t stream) {
   // 79 us against 85; 4096 rotated: 21.9 and 23.5).
   const int64_t bytes = a.T * ((int64_t)a.q_heads + (a.v ? 2 : 1) * a.kv_heads) * a.head_dim * (int64_t)sizeof(T);
   const auto kernel = bytes > ((int64_t)32 << 20) ? rope_kernel<T, EV, INTER, true, 4> : rope_kernel<T, EV, INTER, false, 4>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)gx, gy), dim3(kThreads), lds, stream, a, nt, div_by(units), div_by(hu),
-                     div_by(vu), div_by(half ? half : 1));
+  const Cuts by = {div_by(units), div_by(hu), div_by(vu), div_by(half ? half : 1)};
+  hipLaunchKernelGGL(kernel, dim3((unsigned)gx, gy), dim3(kThreads), lds, stream, a, nt, by);
   return hipGetLastError();
 }
 

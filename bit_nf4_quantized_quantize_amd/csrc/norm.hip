@@ -8,7 +8,7 @@
 // nothing is read twice; 512 elements to a wave (1024 beyond 8192).  Measured:
 // 8192 x 8192 in bfloat16 with every part, forward 108-113 us (4.8-4.95 TB/s,
 // a device copy's rate is 4.9), backward 178 us with the sums (4.5 TB/s); 8191 x
-// 4096 with an fp32 stream, backward 134 us (4.5 TB/s).
+// 4096 with an fp32 stream, backward 132 us (4.6 TB/s).
 #include "decoder.h"
 #include "device.h"
 
@@ -229,6 +229,10 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs a, int t
   __shared__ float buf[2][3][16];
   extern __shared__ __attribute__((aligned(16))) float lds[];  // the gains, at the end the row groups' sums
   constexpr bool LDS_GAINS = NV == 1, AHEAD = NV == 1;
+  // an fp32 row of dxo has no room in flight beside the rest (spills: 65536 x
+  // 256 in fp32 111 us against 82); it is loaded with its own row, whose first
+  // sums do not need it
+  constexpr bool DXO_AHEAD = sizeof(XT) == 2;
   using Row = BwdRow<XT, HT, NV>;
   const int sub = wave_uniform(threadIdx.x / tpr), t = threadIdx.x - sub * tpr, D = a.D;
   const float inv = 1.0f / (float)D;
@@ -245,7 +249,7 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs a, int t
     for (int c = 0; c < NV; ++c) {
       const int j = (c * tpr + t) * 8;
       w.xo[c] = load8<AL>((const XT*)a.x + r * D, j, D);
-      if (a.dxo) w.dxo[c] = load8<AL>((const XT*)a.dxo + r * D, j, D);
+      if (a.dxo && DXO_AHEAD) w.dxo[c] = load8<AL>((const XT*)a.dxo + r * D, j, D);
       if (a.dn) w.dn[c] = load8<AL>((const HT*)a.dn + r * D, j, D);
       if (a.h) w.h[c] = load8<AL>((const HT*)a.h + r * D, j, D);
     }
@@ -280,7 +284,12 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs a, int t
     const int64_t r = r0 + sub;
     const bool mine = r < a.T;
     if (!AHEAD) load(nx, mine ? r : a.T - 1);
-    const Row w = nx;
+    Row w = nx;
+    if (a.dxo && !DXO_AHEAD) {
+#pragma unroll
+      for (int c = 0; c < NV; ++c)
+        w.dxo[c] = load8<AL>((const XT*)a.dxo + (mine ? r : a.T - 1) * D, (c * tpr + t) * 8, D);
+    }
     if (AHEAD && r0 + step < a.T) load(nx, r + step < a.T ? r + step : a.T - 1);
     float s[3] = {0.0f, 0.0f, 0.0f};  // xo^2, a xo, h^2
 #pragma unroll

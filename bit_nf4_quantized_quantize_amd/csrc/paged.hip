@@ -207,6 +207,13 @@ __device__ __forceinline__ Pages pages_at(const AttnArgs& a, const int32_t* tabl
   return p;
 }
 
+// Keeps a wave's LDS accesses before and after it in program order for the
+// compiler; the LDS itself serves a wave's accesses in order.
+__device__ __forceinline__ void lds_in_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // What the lanes of a wave hold of one tile.
 template <int DP>
 struct Tile {
@@ -299,7 +306,7 @@ __global__ __launch_bounds__(64 * W) void paged_attention_kernel(AttnArgs a, int
     const int64_t tok = ti * kTile;
     const bool full = tok + kTile <= n && t.ok[0] && t.ok[1];
     // V to LDS
-    __builtin_amdgcn_wave_barrier();
+    lds_in_order();
 #pragma unroll
     for (int i = 0; i < DP / 16; ++i) {
       const int idx = i * 64 + lane, r = idx / CH, c = idx % CH * 8;
@@ -355,7 +362,7 @@ __global__ __launch_bounds__(64 * W) void paged_attention_kernel(AttnArgs a, int
     for (int j = 0; j < 8; ++j) p[j] -= __uint_as_float((j & 1) ? hi[j >> 1] & 0xFFFF0000u : hi[j >> 1] << 16);
     const uint4 rw = make_uint4(pack_bf2(p[0], p[1]), pack_bf2(p[2], p[3]), pack_bf2(p[4], p[5]), pack_bf2(p[6], p[7]));
     const bf16x8 rb = __builtin_bit_cast(bf16x8, rw);
-    __builtin_amdgcn_wave_barrier();
+    lds_in_order();
 #pragma unroll
     for (int i = 0; i < DP / 16; ++i) {
       const __bf16* src = vt + (4 * g + (col >> 2)) * PITCH + 16 * i + 4 * (col & 3);
@@ -370,7 +377,7 @@ __global__ __launch_bounds__(64 * W) void paged_attention_kernel(AttnArgs a, int
   l += __shfl_xor(l, 16, 64);
   l += __shfl_xor(l, 32, 64);
   if (g == 0) s_m[wave][col] = m, s_l[wave][col] = l;
-  __builtin_amdgcn_wave_barrier();
+  lds_in_order();
   float* ow = reinterpret_cast<float*>(lds + wave * WAVE_BYTES);
 #pragma unroll
   for (int i = 0; i < DP / 16; ++i) *reinterpret_cast<floatx4*>(ow + col * OP + 16 * i + 4 * g) = acc[i];

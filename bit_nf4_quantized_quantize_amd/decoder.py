@@ -165,7 +165,7 @@ def qlora_norm_residual_fwd(x, h=None, w_pre=None, w_post=None, gate=None, alpha
     elif w_pre is not None:
         n = torch.empty_like(x) if nd == xt else torch.empty_like(x, dtype=nd)
     _call("qlora_norm_residual_fwd", x.data_ptr(), _DTYPES[xt], _ptr(h), _DTYPES[nd], x.numel() // D if D else 0, D,
-          _ptr(w_post), _ptr(gate), alpha, _ptr(w_pre), eps, _ptr(xo), _ptr(n), on)
+          _ptr(w_post), _ptr(gate), float(alpha), _ptr(w_pre), float(eps), _ptr(xo), _ptr(n), on)
     return (x if xo is None else xo), n
 
 
@@ -219,7 +219,7 @@ def qlora_norm_residual_bwd(dxo, dn, xo, h=None, w_pre=None, w_post=None, gate=N
         nws = _norm_bwd_workspace(T, D, _DTYPES[xt], _DTYPES[hd])
         ws = torch.empty(nws, dtype=torch.uint8, device=xo.device)
     _call("qlora_norm_residual_bwd", _ptr(dxo), xo.data_ptr(), _DTYPES[xt], _ptr(dn), _ptr(h), _DTYPES[hd], T, D,
-          _ptr(w_post), _ptr(gate), alpha, _ptr(w_pre), eps, dx.data_ptr(), _ptr(dh), _ptr(dw_post), _ptr(dgate),
+          _ptr(w_post), _ptr(gate), float(alpha), _ptr(w_pre), float(eps), dx.data_ptr(), _ptr(dh), _ptr(dw_post), _ptr(dgate),
           _ptr(dw_pre), _ptr(ws), nws, on)
     return NormGrads(dx, dh, dw_pre, dw_post, dgate)
 
@@ -232,8 +232,9 @@ def qlora_rope_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, or
     of the rotated values); see qlora_rope_scaling for `scaling`."""
     if scaling not in ROPE_SCALING:
         raise ValueError(f"scaling must be one of {', '.join(ROPE_SCALING)}")
+    if rot_dim > 1024:
+        raise ValueError("rot_dim must be at most 1024")
     turns, m = (_f64 * max(rot_dim // 2, 1))(), _f32(0.0)
-    lib()
     _call("qlora_rope_frequencies", rot_dim, base, ROPE_SCALING[scaling], factor, original_len, beta_fast, beta_slow,
           turns, ctypes.byref(m))
     return list(turns), m.value
@@ -378,6 +379,8 @@ def qlora_paged_plan(cached_lens, new_lens, free_pages, block_table, page_size, 
     and returns PagedPlan: total_lens [S], starts [S + 1], slots and positions
     [tokens] (rows behind the last new token: -1 and 0) and pages_needed [1],
     parts of one allocation.  `out`: a PagedPlan of these shapes to write to."""
+    if not 0 < page_size < 2 ** 31 or not 0 <= tokens < 2 ** 31:
+        raise ValueError("page_size must be positive and tokens not negative")
     S = cached_lens.shape[0]
     _index(cached_lens, "cached_lens", (S,))
     _index(new_lens, "new_lens", (S,))
@@ -437,5 +440,5 @@ def qlora_paged_attention(q, k_cache, v_cache, block_table, lengths, scale=None,
     nws = _attention_workspace(S, H, kvh, d, cols, page)
     ws = torch.empty(nws, dtype=torch.uint8, device=q.device) if nws else None
     _call("qlora_paged_attention", q.data_ptr(), qs, S, H, kvh, d, k_cache.data_ptr(), v_cache.data_ptr(), pages, page,
-          block_table.data_ptr(), cols, lengths.data_ptr(), scale, out.data_ptr(), _ptr(lse), _ptr(ws), nws, on)
+          block_table.data_ptr(), cols, lengths.data_ptr(), float(scale), out.data_ptr(), _ptr(lse), _ptr(ws), nws, on)
     return out

@@ -280,7 +280,8 @@ class QLoraBlock:
         """The first tokens x [batch, seq, hidden] of the cache's sequences 0 ..
         batch - 1: the block's output, with their keys and values stored."""
         if not self.fused or x.dim() != 3 or x.shape[0] > len(cache.host_lens) or any(cache.host_lens):
-            raise ValueError("prefill needs a fused block, x [batch, seq, hidden] and an empty cache of as many sequences")
+            raise ValueError("prefill needs a fused block, x [batch, seq, hidden] and an empty cache of at least "
+                             "batch sequences")
         b, t, _ = x.shape
         plan = cache.add([t if s < b else 0 for s in range(len(cache.host_lens))])
 

@@ -69,7 +69,8 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = torch._C._cuda_getCurrentRawStream  # what torch.cuda.current_stream wraps, without the object
+_device = torch._C._cuda_getDevice
 
 
 def _here(stream, *tensors):
@@ -86,7 +87,7 @@ def _here(stream, *tensors):
                 if dev is not None:
                     raise ValueError("all tensors of a call must be on one device")
                 dev = i
-    if dev != torch.cuda.current_device():
+    if dev != _device():
         return None
     raw = _raw_stream(dev)
     return raw if stream is None or (stream.cuda_stream == raw and stream.device_index == dev) else None
@@ -116,15 +117,14 @@ def _dense(t, name, shape, dtypes):
                          f"{' or '.join(str(d) for d in dtypes)}")
 
 
+def _new_like(t):
+    """A contiguous tensor of t's shape, type and device."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 def _gain(t, name, shape):
     if t is not None and (t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape}")
-
-
-def _call(name, *args):
-    status = getattr(_lib or lib(), name)(*args)
-    if status:
-        B._check(status, name)
 
 
 # --------------------------------------------------- norm, gate and residual
@@ -164,8 +164,11 @@ def qlora_norm_residual_fwd(x, h=None, w_pre=None, w_post=None, gate=None, alpha
         _dense(n, "n", shape, (nd,))
     elif w_pre is not None:
         n = torch.empty_like(x) if nd == xt else torch.empty_like(x, dtype=nd)
-    _call("qlora_norm_residual_fwd", x.data_ptr(), _DTYPES[xt], _ptr(h), _DTYPES[nd], x.numel() // D if D else 0, D,
-          _ptr(w_post), _ptr(gate), float(alpha), _ptr(w_pre), float(eps), _ptr(xo), _ptr(n), on)
+    status = (_lib or lib()).qlora_norm_residual_fwd(
+        x.data_ptr(), _DTYPES[xt], _ptr(h), _DTYPES[nd], x.numel() // D if D else 0, D, _ptr(w_post), _ptr(gate),
+        float(alpha), _ptr(w_pre), float(eps), _ptr(xo), _ptr(n), on)
+    if status:
+        B._check(status, "qlora_norm_residual_fwd")
     return (x if xo is None else xo), n
 
 
@@ -175,7 +178,10 @@ NormGrads = collections.namedtuple("NormGrads", "dx dh dw_pre dw_post dgate")
 @functools.lru_cache(maxsize=256)
 def _norm_bwd_workspace(T, D, xt, ht):
     nws = _i64(0)
-    _call("qlora_norm_residual_bwd_workspace", T, D, xt, ht, 3, ctypes.byref(nws))
+    status = (_lib or lib()).qlora_norm_residual_bwd_workspace(
+        T, D, xt, ht, 3, ctypes.byref(nws))
+    if status:
+        B._check(status, "qlora_norm_residual_bwd_workspace")
     return nws.value
 
 
@@ -218,9 +224,12 @@ def qlora_norm_residual_bwd(dxo, dn, xo, h=None, w_pre=None, w_post=None, gate=N
         dgate = new() if gate is not None and "gate" in wanted else None
         nws = _norm_bwd_workspace(T, D, _DTYPES[xt], _DTYPES[hd])
         ws = torch.empty(nws, dtype=torch.uint8, device=xo.device)
-    _call("qlora_norm_residual_bwd", _ptr(dxo), xo.data_ptr(), _DTYPES[xt], _ptr(dn), _ptr(h), _DTYPES[hd], T, D,
-          _ptr(w_post), _ptr(gate), float(alpha), _ptr(w_pre), float(eps), dx.data_ptr(), _ptr(dh), _ptr(dw_post), _ptr(dgate),
-          _ptr(dw_pre), _ptr(ws), nws, on)
+    status = (_lib or lib()).qlora_norm_residual_bwd(
+        _ptr(dxo), xo.data_ptr(), _DTYPES[xt], _ptr(dn), _ptr(h), _DTYPES[hd], T, D, _ptr(w_post), _ptr(gate),
+        float(alpha), _ptr(w_pre), float(eps), dx.data_ptr(), _ptr(dh), _ptr(dw_post), _ptr(dgate), _ptr(dw_pre),
+        _ptr(ws), nws, on)
+    if status:
+        B._check(status, "qlora_norm_residual_bwd")
     return NormGrads(dx, dh, dw_pre, dw_post, dgate)
 
 
@@ -235,8 +244,10 @@ def qlora_rope_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, or
     if rot_dim > 1024:
         raise ValueError("rot_dim must be at most 1024")
     turns, m = (_f64 * max(rot_dim // 2, 1))(), _f32(0.0)
-    _call("qlora_rope_frequencies", rot_dim, base, ROPE_SCALING[scaling], factor, original_len, beta_fast, beta_slow,
-          turns, ctypes.byref(m))
+    status = (_lib or lib()).qlora_rope_frequencies(
+        rot_dim, base, ROPE_SCALING[scaling], factor, original_len, beta_fast, beta_slow, turns, ctypes.byref(m))
+    if status:
+        B._check(status, "qlora_rope_frequencies")
     return list(turns), m.value
 
 
@@ -292,7 +303,7 @@ def qlora_rope(q, k, table, positions, inverse=False, q_out=None, k_out=None, st
     if q is not None:
         qh, qs = _heads(q, "q", T, d, dt)
         if q_out is None:
-            q_out, qos = torch.empty(q.shape, dtype=dt, device=q.device), qh * d
+            q_out, qos = _new_like(q), qh * d
         else:
             h, qos = _heads(q_out, "q_out", T, d, dt)
             if h != qh:
@@ -302,16 +313,18 @@ def qlora_rope(q, k, table, positions, inverse=False, q_out=None, k_out=None, st
     if k is not None:
         kh, ks = _heads(k, "k", T, d, dt)
         if k_out is None:
-            k_out, kos = torch.empty(k.shape, dtype=dt, device=k.device), kh * d
+            k_out, kos = _new_like(k), kh * d
         else:
             h, kos = _heads(k_out, "k_out", T, d, dt)
             if h != kh:
                 raise ValueError("k_out must have the heads of k")
     else:
         k_out = None
-    _call("qlora_rope", _ptr(q), qs, qh, _ptr(q_out), qos, _ptr(k), ks, kh, _ptr(k_out), kos, T, d, table.rot_dim,
-          _DTYPES[dt], positions.data_ptr(), table.turns.data_ptr(), table.mscale, table.interleaved, bool(inverse),
-          on)
+    status = (_lib or lib()).qlora_rope(
+        _ptr(q), qs, qh, _ptr(q_out), qos, _ptr(k), ks, kh, _ptr(k_out), kos, T, d, table.rot_dim, _DTYPES[dt],
+        positions.data_ptr(), table.turns.data_ptr(), table.mscale, table.interleaved, bool(inverse), on)
+    if status:
+        B._check(status, "qlora_rope")
     return q_out, k_out
 
 
@@ -356,16 +369,18 @@ def qlora_rope_cache_write(q, k, v, table, positions, slots, k_cache, v_cache, q
     if q is not None:
         qh, qs = _heads(q, "q", T, d, bf)
         if q_out is None:
-            q_out, qos = torch.empty(q.shape, dtype=bf, device=q.device), qh * d
+            q_out, qos = _new_like(q), qh * d
         else:
             h, qos = _heads(q_out, "q_out", T, d, bf)
             if h != qh:
                 raise ValueError("q_out must have the heads of q")
     else:
         q_out = None
-    _call("qlora_rope_cache_write", _ptr(q), qs, qh, _ptr(q_out), qos, k.data_ptr(), ks, v.data_ptr(), vs, kvh, T, d,
-          rot, _ptr(positions), _ptr(turns), mscale, inter, slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          pages, page, on)
+    status = (_lib or lib()).qlora_rope_cache_write(
+        _ptr(q), qs, qh, _ptr(q_out), qos, k.data_ptr(), ks, v.data_ptr(), vs, kvh, T, d, rot, _ptr(positions),
+        _ptr(turns), mscale, inter, slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), pages, page, on)
+    if status:
+        B._check(status, "qlora_rope_cache_write")
     return q_out
 
 
@@ -394,22 +409,26 @@ def qlora_paged_plan(cached_lens, new_lens, free_pages, block_table, page_size, 
             return qlora_paged_plan(cached_lens, new_lens, free_pages, block_table, page_size, tokens, out)
     if out is None:
         sizes = (S, S + 1, tokens, tokens, 1)
-        out = PagedPlan(*torch.empty(2 * (S + tokens + 1), dtype=torch.int32, device=cached_lens.device)
-                        .split_with_sizes(sizes))
+        out = PagedPlan._make(cached_lens.new_empty(2 * (S + tokens + 1)).split_with_sizes(sizes))
     else:
         for name, n in zip(PagedPlan._fields, (S, S + 1, tokens, tokens, 1)):
             _index(getattr(out, name), name, (n,))
     total, starts, slots, positions, needed = out
-    _call("qlora_paged_plan", cached_lens.data_ptr(), new_lens.data_ptr(), S, page_size, free_pages.data_ptr(), nfree,
-          block_table.data_ptr(), cols, tokens, total.data_ptr(), starts.data_ptr(), slots.data_ptr(),
-          positions.data_ptr(), needed.data_ptr(), on)
+    status = (_lib or lib()).qlora_paged_plan(
+        cached_lens.data_ptr(), new_lens.data_ptr(), S, page_size, free_pages.data_ptr(), nfree, block_table.data_ptr(),
+        cols, tokens, total.data_ptr(), starts.data_ptr(), slots.data_ptr(), positions.data_ptr(), needed.data_ptr(), on)
+    if status:
+        B._check(status, "qlora_paged_plan")
     return out
 
 
 @functools.lru_cache(maxsize=256)
 def _attention_workspace(S, H, kvh, d, cols, page):
     nws = _i64(0)
-    _call("qlora_paged_attention_workspace", S, H, kvh, d, cols, page, ctypes.byref(nws))
+    status = (_lib or lib()).qlora_paged_attention_workspace(
+        S, H, kvh, d, cols, page, ctypes.byref(nws))
+    if status:
+        B._check(status, "qlora_paged_attention_workspace")
     return nws.value
 
 
@@ -432,13 +451,16 @@ def qlora_paged_attention(q, k_cache, v_cache, block_table, lengths, scale=None,
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((S, H, d), dtype=torch.bfloat16, device=q.device)
+        out = _new_like(q)
     else:
         _dense(out, "out", (S, H, d), _BF16)
     if lse is not None:
         _dense(lse, "lse", (S, H), (torch.float32,))
     nws = _attention_workspace(S, H, kvh, d, cols, page)
-    ws = torch.empty(nws, dtype=torch.uint8, device=q.device) if nws else None
-    _call("qlora_paged_attention", q.data_ptr(), qs, S, H, kvh, d, k_cache.data_ptr(), v_cache.data_ptr(), pages, page,
-          block_table.data_ptr(), cols, lengths.data_ptr(), float(scale), out.data_ptr(), _ptr(lse), _ptr(ws), nws, on)
+    ws = q.new_empty(nws // 2) if nws else None  # in q's elements of two bytes
+    status = (_lib or lib()).qlora_paged_attention(
+        q.data_ptr(), qs, S, H, kvh, d, k_cache.data_ptr(), v_cache.data_ptr(), pages, page, block_table.data_ptr(),
+        cols, lengths.data_ptr(), float(scale), out.data_ptr(), _ptr(lse), _ptr(ws), nws, on)
+    if status:
+        B._check(status, "qlora_paged_attention")
     return out

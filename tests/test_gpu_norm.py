@@ -234,3 +234,50 @@ def test_other_stream_and_graph(D):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(ref, out)), k
+
+
+def test_offsets_beyond_32_bits(D):
+    """More than 2^32 elements: the last rows equal a call on them alone."""
+    _log("norm 64-bit offsets")
+    T, W = 2 ** 19 + 5, 8192
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.zeros(T, W, dtype=BF, device="cuda")
+    h, dxo = torch.zeros_like(x), torch.zeros_like(x)
+    for t in (x, h, dxo):
+        t[-5:] = torch.randn(5, W, generator=g, device="cuda").to(BF)
+    w = 1 + 0.1 * torch.randn(W, generator=g, device="cuda")
+    kw = dict(w_pre=w, w_post=w, alpha=0.5)
+    xo, n = D.qlora_norm_residual_fwd(x, h, **kw)
+    ref = D.qlora_norm_residual_fwd(x[-5:].clone(), h[-5:].clone(), **kw)
+    assert torch.equal(xo[-5:], ref[0]) and torch.equal(n[-5:], ref[1]) and not xo[:-5].any()
+    last = [t[-5:].clone() for t in (dxo, h, xo)]
+    got = D.qlora_norm_residual_bwd(dxo, h, xo, h, dx=dxo, **kw)   # in place
+    ref = D.qlora_norm_residual_bwd(last[0], last[1], last[2], last[1], **kw)
+    assert torch.equal(got.dx[-5:], ref.dx) and torch.equal(got.dh[-5:], ref.dh)
+    assert not got.dx[:-5].any() and not got.dh[:-5].any()
+
+
+def test_views_that_start_off_a_16_byte_boundary_are_refused(D):
+    from bit_nf4_quantized_quantize_amd import binding
+    x = torch.zeros(9 * 64, dtype=BF, device="cuda")[1:1 + 8 * 64].view(8, 64)
+    w = torch.ones(64, device="cuda")
+    with pytest.raises(binding.QLoraError) as e:
+        D.qlora_norm_residual_fwd(x, None, w_pre=w)
+    assert e.value.status == binding.QLORA_ERR_MISALIGNED
+
+
+def test_leading_dimensions_and_extremes_of_the_scalars(D):
+    _log("norm shapes and scalars")
+    x, h, w_pre, w_post, gt, dxo, dn = _inputs(12, 96, F, BF, True, True, seed=21)
+    kw = dict(w_pre=w_pre, w_post=w_post, gate=gt)
+    ref = D.qlora_norm_residual_fwd(x, h, **kw)
+    got = D.qlora_norm_residual_fwd(x.view(2, 3, 2, 96), h.view(2, 3, 2, 96), **kw)
+    assert got[0].shape == (2, 3, 2, 96) and torch.equal(got[0].view(12, 96), ref[0])
+    one = D.qlora_norm_residual_fwd(x[3], h[3], **kw)
+    assert one[0].shape == (96,) and torch.equal(one[1], ref[1][3])
+    assert torch.equal(D.qlora_norm_residual_fwd(x, h, alpha=0.0, **kw)[0], x)
+    xo, n = D.qlora_norm_residual_fwd(x, h, eps=0.0, alpha=-2.0, **kw)
+    rx, rn = od.norm_residual(_n(x), _n(h), _n(w_pre), _n(w_post), _n(gt), -2.0, 0.0)
+    E = C * U * (np.abs(_n(x)) + np.abs(rx - _n(x)))
+    _close(xo, rx, E, F, "xo")
+    _close(n, rn, (E + C * U * np.abs(rx)) / od.rms(rx, 0.0) * np.abs(_n(w_pre)), BF, "n")

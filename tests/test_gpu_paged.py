@@ -316,6 +316,21 @@ def test_plan_lengths_beyond_31_bits(D):
     assert t.tolist() == [[4, -7, -7]]
 
 
+def test_plan_into_given_buffers(D):
+    _log("plan out=")
+    rng = np.random.default_rng(11)
+    cached, new, free, table = _plan_case(rng, 20, 16, 50, 30, 5)
+    T = int(new.sum()) + 4
+    e = lambda n: torch.full((n,), -9, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = D.PagedPlan(e(20), e(21), e(T), e(T), e(1))
+    assert _check_plan(D, cached, new, free, table, 16, T, out=out) is out
+    with pytest.raises(ValueError):
+        D.qlora_paged_plan(_dev(cached), _dev(new), _dev(free), _dev(table), 16, T, out=out._replace(slots=e(T - 1)))
+    for page, tokens in ((0, T), (-1, T), (2 ** 32 + 16, T), (16, -1)):
+        with pytest.raises(ValueError):
+            D.qlora_paged_plan(_dev(cached), _dev(new), _dev(free), _dev(table), page, tokens)
+
+
 def test_plan_graph(D):
     _log("plan graph")
     rng = np.random.default_rng(5)

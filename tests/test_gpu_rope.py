@@ -250,3 +250,32 @@ def test_other_stream_and_graph(D):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(ref, out + (kc, vc))), n
+
+
+def test_offsets_beyond_32_bits(D):
+    """More than 2^32 elements of q: the last tokens equal a call on them alone."""
+    _log("rope 64-bit offsets")
+    T, H, d = 2 ** 19 + 3, 64, 128
+    q = torch.zeros(T, H, d, dtype=BF, device="cuda")
+    q[-3:] = torch.randn(3, H, d, device="cuda").to(BF)
+    tab = D.RopeTable(d, device="cuda")
+    pos = torch.arange(T, device="cuda", dtype=torch.int32)
+    ref, _ = D.qlora_rope(q[-3:].clone(), None, tab, pos[-3:].clone())
+    out, _ = D.qlora_rope(q, None, tab, pos, q_out=q)
+    assert torch.equal(out[-3:], ref) and not out[:-3].any()
+
+
+def test_cache_write_from_slices_and_in_place(D):
+    """q, k and v as slices of one projection, q rotated where it lies."""
+    _log("cache write from slices")
+    g = torch.Generator(device="cuda").manual_seed(8)
+    T, H, KV, d, page, pages = 21, 6, 2, 64, 16, 4
+    tab = D.RopeTable(48, device="cuda")
+    pos = torch.arange(T, device="cuda", dtype=torch.int32) + 5
+    slots = torch.randperm(page * pages, generator=g, device="cuda")[:T].to(torch.int32)
+    full = _randn(g, T, (H + 2 * KV) * d, dtype=BF)
+    q, k, v = (full[:, a * d:b * d].view(T, b - a, d) for a, b in ((0, H), (H, H + KV), (H + KV, H + 2 * KV)))
+    c = [torch.zeros(pages, KV, page, d, dtype=BF, device="cuda") for _ in range(4)]
+    ref = D.qlora_rope_cache_write(q.clone(), k.clone(), v.clone(), tab, pos, slots, c[0], c[1])
+    got = D.qlora_rope_cache_write(q, k, v, tab, pos, slots, c[2], c[3], q_out=q)
+    assert got is q and torch.equal(q, ref) and torch.equal(c[0], c[2]) and torch.equal(c[1], c[3])

@@ -37,7 +37,7 @@ struct NormArgs {
   const float* w_post;
   const float* gate;
   const float* w_pre;
-  float* part;     // backward: [3][norm_bwd_parts][D] partial sums (dw_post, dgate, dw_pre), or NULL
+  float* part;     // backward: [2][norm_bwd_parts][D] partial sums (dx y and dn xo r), or NULL
   float* dw_post;
   float* dgate;
   float* dw_pre;

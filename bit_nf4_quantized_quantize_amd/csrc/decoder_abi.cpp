@@ -62,7 +62,7 @@ int check_rows(int64_t T, int64_t D, float eps, const char* fn) {
   return QLORA_OK;
 }
 
-int64_t norm_ws(int64_t T, int64_t D) { return T == 0 ? 0 : 3 * norm_bwd_parts(T, D) * D * 4; }
+int64_t norm_ws(int64_t T, int64_t D) { return T == 0 ? 0 : 2 * norm_bwd_parts(T, D) * D * 4; }
 
 // Sizes and strides of a rotary call.
 int check_rope(int64_t q_stride, int32_t q_heads, int64_t qo_stride, int64_t k_stride, int32_t kv_heads, int64_t T,

@@ -7,8 +7,8 @@
 // row is held in the registers of its threads (NV chunks of 8 elements each), so
 // nothing is read twice; 512 elements to a wave (1024 beyond 8192).  Measured:
 // 8192 x 8192 in bfloat16 with every part, forward 108-113 us (4.8-4.95 TB/s,
-// a device copy's rate is 4.9), backward 178 us with the sums (4.5 TB/s); 8191 x
-// 4096 with an fp32 stream, backward 132 us (4.6 TB/s).
+// a device copy's rate is 4.9), backward 174 us with the sums (4.6 TB/s); 8191 x
+// 4096 with an fp32 stream, backward 127 us (4.75 TB/s).
 #include "decoder.h"
 #include "device.h"
 
@@ -221,7 +221,9 @@ struct BwdRow {
 // once per workgroup; norm_sums_kernel adds those.  The gains lie in LDS for the
 // whole walk: registers have no room for them beside the sums, the row and the
 // next row, and from the L2 they would double its reads.  Rows beyond 8192
-// (NV = 2) have no room for either, and no next row in flight.
+// (NV = 2) keep the sums in the LDS and read the row and the gains where they are
+// used, from the caches after the first time (all in registers spilled: 4096 x
+// 16384 in bfloat16 839 us).
 constexpr int kBwdThreads = 1024;
 
 template <typename XT, typename HT, int NV, bool AL, bool SUMS>
@@ -237,13 +239,26 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs a, int t
   const int sub = wave_uniform(threadIdx.x / tpr), t = threadIdx.x - sub * tpr, D = a.D;
   const float inv = 1.0f / (float)D;
   int turn = 0;
-  float sp[NV][8], sg[NV][8], sw[NV][8];
+  // sums of dx y and of dn xo r: in registers, or in the thread's own places of
+  // the LDS
+  constexpr bool LDS_SUMS = SUMS && NV == 2;
+  float sums[2][NV][8];
+  auto place = [&](int which, int c, int i) { return ((which * NV + c) * 8 + i) * tpr + t; };
   if (SUMS) {
 #pragma unroll
-    for (int c = 0; c < NV; ++c)
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sp[c][i] = sg[c][i] = sw[c][i] = 0.0f;
+      for (int c = 0; c < NV; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          sums[k][c][i] = 0.0f;
+          if (LDS_SUMS) lds[place(k, c, i)] = 0.0f;
+        }
   }
+  auto add = [&](int which, int c, int i, float u, float v) {
+    if (LDS_SUMS) lds[place(which, c, i)] = __builtin_fmaf(u, v, lds[place(which, c, i)]);
+    else sums[which][c][i] = __builtin_fmaf(u, v, sums[which][c][i]);
+  };
   auto load = [&](Row& w, int64_t r) {
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
@@ -281,31 +296,52 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs a, int t
   int64_t r0 = (int64_t)blockIdx.x * rows;
   if (AHEAD) load(nx, r0 + sub < a.T ? r0 + sub : a.T - 1);
   for (; r0 < a.T; r0 += step) {
-    const int64_t r = r0 + sub;
+    const int64_t r = r0 + sub, rr = r < a.T ? r : a.T - 1;
     const bool mine = r < a.T;
-    if (!AHEAD) load(nx, mine ? r : a.T - 1);
-    Row w = nx;
-    if (a.dxo && !DXO_AHEAD) {
+    Row w;
+    if (AHEAD) {
+      w = nx;
+      if (a.dxo && !DXO_AHEAD) {
 #pragma unroll
-      for (int c = 0; c < NV; ++c)
-        w.dxo[c] = load8<AL>((const XT*)a.dxo + (mine ? r : a.T - 1) * D, (c * tpr + t) * 8, D);
+        for (int c = 0; c < NV; ++c) w.dxo[c] = load8<AL>((const XT*)a.dxo + rr * D, (c * tpr + t) * 8, D);
+      }
+      if (r0 + step < a.T) load(nx, r + step < a.T ? r + step : a.T - 1);
     }
-    if (AHEAD && r0 + step < a.T) load(nx, r + step < a.T ? r + step : a.T - 1);
+    // chunk c of the row: held, or (NV = 2) loaded where it is used
+    auto xo_of = [&](int c) -> decltype(auto) {
+      if constexpr (AHEAD) return (w.xo[c]);
+      else return load8<AL>((const XT*)a.x + rr * D, (c * tpr + t) * 8, D);
+    };
+    auto dxo_of = [&](int c) -> decltype(auto) {
+      if constexpr (AHEAD) return (w.dxo[c]);
+      else return a.dxo ? load8<AL>((const XT*)a.dxo + rr * D, (c * tpr + t) * 8, D) : Raw8<XT>{};
+    };
+    auto dn_of = [&](int c) -> decltype(auto) {
+      if constexpr (AHEAD) return (w.dn[c]);
+      else return load8<AL>((const HT*)a.dn + rr * D, (c * tpr + t) * 8, D);
+    };
+    auto h_of = [&](int c) -> decltype(auto) {
+      if constexpr (AHEAD) return (w.h[c]);
+      else return a.h ? load8<AL>((const HT*)a.h + rr * D, (c * tpr + t) * 8, D) : Raw8<HT>{};
+    };
     float s[3] = {0.0f, 0.0f, 0.0f};  // xo^2, a xo, h^2
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
       if (a.dn) {
         const Raw8<float> wp = gain(0, c);
+        const Raw8<XT>& xo = xo_of(c);
+        const Raw8<HT>& dn = dn_of(c);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float x = w.xo[c].get(i);
+          const float x = xo.get(i);
           s[0] = __builtin_fmaf(x, x, s[0]);
-          s[1] = __builtin_fmaf(w.dn[c].get(i) * wp.get(i), x, s[1]);
+          s[1] = __builtin_fmaf(dn.get(i) * wp.get(i), x, s[1]);
         }
       }
       if (a.w_post) {
+        const Raw8<HT>& h = h_of(c);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[2] = __builtin_fmaf(w.h[c].get(i), w.h[c].get(i), s[2]);
+        for (int i = 0; i < 8; ++i) s[2] = __builtin_fmaf(h.get(i), h.get(i), s[2]);
       }
     }
     row_sum<3>(s, buf, turn, tpr);
@@ -317,28 +353,31 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs a, int t
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
       const int j = (c * tpr + t) * 8;
+      const Raw8<XT>& dxo = dxo_of(c);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[c][i] = a.dxo ? w.dxo[c].get(i) : 0.0f;
+      for (int i = 0; i < 8; ++i) g[c][i] = a.dxo ? dxo.get(i) : 0.0f;
       if (a.dn) {
         const Raw8<float> wp = gain(0, c);
+        const Raw8<XT>& xo = xo_of(c);
+        const Raw8<HT>& dn = dn_of(c);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float x = w.xo[c].get(i), d = w.dn[c].get(i);
+          const float x = xo.get(i), d = dn.get(i);
           g[c][i] = __builtin_fmaf(rs, __builtin_fmaf(d, wp.get(i), -(x * back)), g[c][i]);
-          if (SUMS && mine) sw[c][i] = __builtin_fmaf(d, x * rs, sw[c][i]);
+          if (SUMS && mine) add(1, c, i, d, x * rs);
         }
       }
       if (mine) store8<AL>((XT*)a.xo + r * D, g[c], j, D);
       Raw8<float> wp, gt;
       if (a.w_post) wp = gain(1, c);
       if (a.gate) gt = gain(2, c);
+      const Raw8<HT>& h = h_of(c);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float y = a.h ? w.h[c].get(i) * rh : 0.0f;
+        const float y = a.h ? h.get(i) * rh : 0.0f;
         float b = g[c][i] * a.alpha;
-        if (SUMS && mine) sg[c][i] = __builtin_fmaf(b, a.w_post ? y * wp.get(i) : y, sg[c][i]);
+        if (SUMS && mine) add(0, c, i, g[c][i], y);
         if (a.gate) b *= gt.get(i);
-        if (SUMS && mine) sp[c][i] = __builtin_fmaf(b, y, sp[c][i]);
         if (a.w_post) b *= wp.get(i);
         q[0] = __builtin_fmaf(b, y, q[0]);
         g[c][i] = b;
@@ -349,9 +388,11 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs a, int t
         row_sum<1>(q, buf, turn, tpr);
         const float m = q[0] * inv;
 #pragma unroll
-        for (int c = 0; c < NV; ++c)
+        for (int c = 0; c < NV; ++c) {
+          const Raw8<HT>& h = h_of(c);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) g[c][i] = rh * (g[c][i] - w.h[c].get(i) * rh * m);
+          for (int i = 0; i < 8; ++i) g[c][i] = rh * (g[c][i] - h.get(i) * rh * m);
+        }
       }
       if (mine) {
 #pragma unroll
@@ -360,8 +401,14 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs a, int t
     }
   }
   if (SUMS) {
-    auto flush = [&](float (&v)[NV][8], int which) {
-      if (rows > 1) {  // add the row groups' sums, in order
+    auto flush = [&](int which) {
+      float(&v)[NV][8] = sums[which];
+      if (LDS_SUMS) {
+#pragma unroll
+        for (int c = 0; c < NV; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[c][i] = lds[place(which, c, i)];
+      } else if (rows > 1) {  // add the row groups' sums, in order
         __syncthreads();
 #pragma unroll
         for (int c = 0; c < NV; ++c)
@@ -382,18 +429,19 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormArgs a, int t
         for (int c = 0; c < NV; ++c) store8<AL>(row, v[c], (c * tpr + t) * 8, D);
       }
     };
-    if (a.dw_post) flush(sp, 0);
-    if (a.dgate) flush(sg, 1);
-    if (a.dw_pre) flush(sw, 2);
+    if (a.dw_post || a.dgate) flush(0);
+    if (a.dw_pre) flush(1);
   }
 }
 
-// The three sums over tokens from the partial sums, in a fixed order: a
-// workgroup takes 64 columns, its wave w the partials w, w + 16, ...
+// The gradients of the gains and the gate from the partial sums, added in a
+// fixed order: a workgroup takes 64 columns, its wave w the partials w, w + 16,
+// ...  One sum, of dx y, serves two of them: dw_post = alpha gate sum and dgate =
+// alpha w_post sum.
 __global__ __launch_bounds__(1024) void norm_sums_kernel(NormArgs a, int64_t parts) {
   __shared__ float s[16][64];
-  float* out = blockIdx.y == 0 ? a.dw_post : blockIdx.y == 1 ? a.dgate : a.dw_pre;
-  if (!out) return;
+  const bool pre = blockIdx.y != 0;
+  if (pre ? !a.dw_pre : !a.dw_post && !a.dgate) return;
   const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
   const int64_t col = (int64_t)blockIdx.x * 64 + l;
   float acc = 0.0f;
@@ -407,7 +455,13 @@ __global__ __launch_bounds__(1024) void norm_sums_kernel(NormArgs a, int64_t par
   if (w == 0 && col < a.D) {
 #pragma unroll
     for (int k = 1; k < 16; ++k) acc += s[k][l];
-    out[col] = acc;
+    if (pre) {
+      a.dw_pre[col] = acc;
+    } else {
+      acc *= a.alpha;
+      if (a.dw_post) a.dw_post[col] = a.gate ? acc * a.gate[col] : acc;
+      if (a.dgate) a.dgate[col] = a.w_post ? acc * a.w_post[col] : acc;
+    }
   }
 }
 
@@ -425,18 +479,10 @@ int row_threads(int64_t D) {
   return (int)((D + each - 1) / each) * 64;
 }
 
-// How the backward walks: `rows` at a time per workgroup, `groups` workgroups
-// at most.  One workgroup of up to 1024 threads per CU; with many rows of up to
-// 4096, two of up to 512, whose barriers do not meet (8191 x 4096: 139 and 134
-// us; 8192 x 2048: 51 and 49; but twice the partial sums, 300 x 4096: 19.5 and
-// 23.6 us, so only from 8 rows per workgroup on).
-struct Walk {
-  int rows, groups;
-};
-Walk walk_of(int64_t T, int64_t D) {
-  const bool two = D <= 4096 && T >= 8 * 512;
-  return {(two ? 512 : kBwdThreads) / row_threads(D), two ? 512 : 256};
-}
+// The backward: one workgroup per CU at most, with as many rows at a time as
+// 1024 threads hold.
+constexpr int kBwdGroups = 256;
+int bwd_rows(int64_t D) { return kBwdThreads / row_threads(D); }
 
 template <typename XT, typename HT>
 hipError_t fwd_types(const NormArgs& a, hipStream_t stream) {
@@ -452,14 +498,16 @@ hipError_t fwd_types(const NormArgs& a, hipStream_t stream) {
 
 template <typename XT, typename HT, int NV, bool AL>
 hipError_t bwd_as(const NormArgs& a, hipStream_t stream) {
-  const int tpr = row_threads(a.D), rows = walk_of(a.T, a.D).rows;
+  const int tpr = row_threads(a.D), rows = bwd_rows(a.D);
   const int64_t parts = norm_bwd_parts(a.T, a.D);
   const bool sums = a.dw_post || a.dgate || a.dw_pre;
-  const size_t gains = NV == 1 ? 3 * (size_t)tpr * 32 : 0, add = sums && rows > 1 ? (size_t)rows * tpr * NV * 32 : 0;
+  // NV = 1: the gains, then the row groups' sums; NV = 2 (one row): the sums
+  const size_t gains = NV == 1 ? 3 * (size_t)tpr * 32 : 0;
+  const size_t add = !sums ? 0 : NV == 2 ? 2 * (size_t)tpr * NV * 32 : rows > 1 ? (size_t)rows * tpr * 32 : 0;
   const auto kernel = sums ? norm_bwd_kernel<XT, HT, NV, AL, true> : norm_bwd_kernel<XT, HT, NV, AL, false>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)parts), dim3(tpr * rows), gains > add ? gains : add, stream, a, tpr, rows);
   if (sums)
-    hipLaunchKernelGGL(norm_sums_kernel, dim3((unsigned)((a.D + 63) / 64), 3), dim3(1024), 0, stream, a, parts);
+    hipLaunchKernelGGL(norm_sums_kernel, dim3((unsigned)((a.D + 63) / 64), 2), dim3(1024), 0, stream, a, parts);
   return hipGetLastError();
 }
 
@@ -473,9 +521,8 @@ hipError_t bwd_types(const NormArgs& a, hipStream_t stream) {
 }  // namespace
 
 int64_t norm_bwd_parts(int64_t T, int64_t D) {
-  const Walk w = walk_of(T, D);
-  const int64_t groups = (T + w.rows - 1) / w.rows;
-  return groups < w.groups ? groups : w.groups;
+  const int64_t rows = bwd_rows(D), groups = (T + rows - 1) / rows;
+  return groups < kBwdGroups ? groups : kBwdGroups;
 }
 
 hipError_t launch_norm_fwd(const NormArgs& a, bool x_f32, bool h_f32, hipStream_t stream) {

@@ -31,7 +31,7 @@ int paged_splits(int64_t S, int, int kv, int, int64_t len) { return S > 0 && len
 hipError_t launch_norm_fwd(const NormArgs&, bool, bool, hipStream_t) { return ++g_launches, hipSuccess; }
 hipError_t launch_norm_bwd(const NormArgs& a, bool, bool, hipStream_t) {
   ++g_launches;
-  if (a.T && (a.dw_post || a.dgate || a.dw_pre)) inside(a.part, 3 * norm_bwd_parts(a.T, a.D) * a.D * 4, "norm partials");
+  if (a.T && (a.dw_post || a.dgate || a.dw_pre)) inside(a.part, 2 * norm_bwd_parts(a.T, a.D) * a.D * 4, "norm partials");
   return hipSuccess;
 }
 hipError_t launch_rope(const RopeArgs& a, bool, hipStream_t) {

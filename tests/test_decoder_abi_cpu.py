@@ -74,7 +74,7 @@ def test_norm_backward_refusals():
         assert f(**{k: MIS}) == AL, k
     n = ctypes.c_int64()
     g = D.lib().qlora_norm_residual_bwd_workspace
-    assert g(2, 64, F32, BF16, 3, ctypes.byref(n)) == OK and n.value >= 3 * 64 * 4
+    assert g(2, 64, F32, BF16, 3, ctypes.byref(n)) == OK and n.value >= 2 * 64 * 4
     assert f(nws=n.value - 1) == WS and f(ws=None) == BAD
     assert g(2, 64, F32, BF16, 0, ctypes.byref(n)) == OK and n.value == 0
     assert g(0, 64, F32, BF16, 3, ctypes.byref(n)) == OK and n.value == 0

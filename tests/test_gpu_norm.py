@@ -148,7 +148,7 @@ def test_parts_left_out(D):
 
 def test_in_place(D):
     _log("norm in place")
-    for W in (200, 4096, 4099):
+    for W in (200, 4096, 4099, 12290):
         x, h, w_pre, w_post, gt, dxo, dn = _inputs(9, W, BF, BF, True, True, seed=W)
         xo, n = D.qlora_norm_residual_fwd(x, h, w_pre=w_pre, w_post=w_post, gate=gt)
         x2 = x.clone()
@@ -160,7 +160,7 @@ def test_in_place(D):
         assert torch.equal(a.dx, d2) and torch.equal(a.dh, n3) and b.dx is d2
 
 
-@pytest.mark.parametrize("T,W", [(3000, 256), (1111, 1024), (700, 4096), (600, 8192)])
+@pytest.mark.parametrize("T,W", [(3000, 256), (1111, 1024), (700, 4096), (600, 8192), (600, 16384), (270, 9001), (301, 1536)])
 def test_many_tokens_sums(D, T, W):
     """More rows than workgroups keep sums for, and results that repeat."""
     _log(f"norm sums T={T} W={W}")

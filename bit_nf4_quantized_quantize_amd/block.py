@@ -92,6 +92,15 @@ class QLoraLinear:
         return sum(self.qw.sizes.values())
 
 
+def _dense16(t):
+    """t (or None) contiguous and on a 16-byte boundary, as the library takes it
+    (a contiguous slice of a larger tensor may start off one)."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _NormResidualFn(torch.autograd.Function):
     """qlora_norm_residual_fwd with its backward."""
 
@@ -111,8 +120,7 @@ class _NormResidualFn(torch.autograd.Function):
             return (None,) * 8
         xo, h, w_pre, w_post, gate = ctx.saved_tensors
         ht, alpha, eps = ctx.args
-        dxo = None if dxo is None else dxo.contiguous()
-        dn = None if dn is None else dn.contiguous()
+        dxo, dn = _dense16(dxo), _dense16(dn)
         need = ctx.needs_input_grad
         gains = [name for i, name in ((2, "w_pre"), (3, "w_post"), (4, "gate")) if need[i]]
         if xo is None:
@@ -126,8 +134,7 @@ class _NormResidualFn(torch.autograd.Function):
 def norm_residual(x, h=None, w_pre=None, w_post=None, gate=None, alpha=1.0, eps=EPS, n_dtype=torch.bfloat16):
     """Differentiable qlora_norm_residual_fwd: (xo, n).  Without h, xo is x and n
     has n_dtype; without w_pre, n is None."""
-    return _NormResidualFn.apply(x.contiguous(), None if h is None else h.contiguous(), w_pre, w_post, gate, alpha, eps,
-                                 n_dtype)
+    return _NormResidualFn.apply(_dense16(x), _dense16(h), w_pre, w_post, gate, alpha, eps, n_dtype)
 
 
 class _RopeFn(torch.autograd.Function):
@@ -135,19 +142,22 @@ class _RopeFn(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, table, positions):
-        ctx.args = (table, positions)
+        ctx.table = table
+        ctx.save_for_backward(positions, table.turns)   # as they are now: a later change is noticed
+        ctx.set_materialize_grads(False)
         return D.qlora_rope(q, k, table, positions)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dq, dk):
-        table, positions = ctx.args
-        dq, dk = D.qlora_rope(dq.contiguous(), dk.contiguous(), table, positions, inverse=True)
+        if dq is not None or dk is not None:
+            dq, dk = D.qlora_rope(_dense16(dq), _dense16(dk), ctx.table, ctx.saved_tensors[0], inverse=True)
         return dq, dk, None, None
 
 
 def rope(q, k, table, positions):
-    """Differentiable qlora_rope of q and k [T, heads, head_dim]."""
+    """Differentiable qlora_rope of q and k [T, heads, head_dim] (either may be
+    None)."""
     return _RopeFn.apply(q, k, table, positions)
 
 
@@ -156,10 +166,13 @@ class PagedCache:
     up to `max_len` tokens: bfloat16 pages [num_pages, heads, page_size,
     head_dim] of keys and values, the block table, and the pages not in use.
     The lengths are known to the host too, so running out of room raises
-    before anything is enqueued."""
+    before anything is enqueued.  page_size is a power of two from 16 to 1024,
+    head_dim a multiple of 8 up to 256, as the attention takes them."""
 
     def __init__(self, num_pages, page_size, heads, head_dim, max_seqs, max_len, device=None):
         dev = device if device is not None else torch.device("cuda", torch.cuda.current_device())
+        if page_size not in (16, 32, 64, 128, 256, 512, 1024) or head_dim % 8 or not 8 <= head_dim <= 256:
+            raise ValueError("page_size must be a power of two in [16, 1024], head_dim a multiple of 8 in [8, 256]")
         shape = (num_pages, heads, page_size, head_dim)
         self.k = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
         self.v = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
@@ -275,13 +288,24 @@ class QLoraBlock:
         return PagedCache(num_pages, page_size, self.heads, self.hidden // self.heads, max_seqs, max_len,
                           self.lin["q"].A.device)
 
+    def _check_cached(self, x, cache):
+        """Everything a cached call needs, before the cache is touched."""
+        d = self.hidden // self.heads
+        if not self.fused:
+            raise ValueError("the cache needs a block in the fused form")
+        if x.dtype not in (torch.float32, torch.bfloat16) or x.device != cache.k.device:
+            raise ValueError("x must be float32 or bfloat16 and on the cache's device")
+        if cache.k.shape[1] != self.heads or cache.k.shape[3] != d:
+            raise ValueError(f"the cache must hold {self.heads} heads of {d}")
+
     @torch.no_grad()
     def prefill(self, x, cache):
         """The first tokens x [batch, seq, hidden] of the cache's sequences 0 ..
         batch - 1: the block's output, with their keys and values stored."""
-        if not self.fused or x.dim() != 3 or x.shape[0] > len(cache.host_lens) or any(cache.host_lens):
-            raise ValueError("prefill needs a fused block, x [batch, seq, hidden] and an empty cache of at least "
-                             "batch sequences")
+        self._check_cached(x, cache)
+        if x.dim() != 3 or x.shape[2] != self.hidden or x.shape[0] > len(cache.host_lens) or any(cache.host_lens):
+            raise ValueError(f"prefill needs x [batch, seq, {self.hidden}] and an empty cache of at least batch "
+                             "sequences")
         b, t, _ = x.shape
         plan = cache.add([t if s < b else 0 for s in range(len(cache.host_lens))])
 
@@ -299,8 +323,9 @@ class QLoraBlock:
         """One more token x [sequences, hidden] for every sequence of the cache:
         the block's output."""
         S = len(cache.host_lens)
-        if not self.fused or tuple(x.shape) != (S, self.hidden):
-            raise ValueError(f"decode needs a fused block and x [{S}, {self.hidden}]")
+        self._check_cached(x, cache)
+        if tuple(x.shape) != (S, self.hidden):
+            raise ValueError(f"decode needs x [{S}, {self.hidden}]")
         plan = cache.add([1] * S)
 
         def attend(q, k, v):

@@ -196,3 +196,90 @@ def test_second_derivatives_are_refused(BL):
     (gx,) = torch.autograd.grad(n.sum(), x, create_graph=True)
     with pytest.raises(RuntimeError):
         gx.sum().backward()
+
+
+def test_rope_autograd(BL):
+    """Gradients of q alone, of k alone and of both; positions changed between
+    forward and backward are noticed."""
+    _log("rope autograd")
+    from bit_nf4_quantized_quantize_amd import RopeTable
+    tab = RopeTable(32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q, k = (torch.randn(7, h, 64, generator=g, device="cuda") for h in (4, 2))
+    w = torch.randn(7, 4, 64, generator=g, device="cuda")
+    pos = torch.arange(7, device="cuda", dtype=torch.int32) * 100
+
+    def grads(use_q, use_k, loss_q, loss_k):
+        ql, kl = (z.clone().requires_grad_(True) if u else None for z, u in ((q, use_q), (k, use_k)))
+        qo, ko = BL.rope(ql, kl, tab, pos)
+        loss = 0
+        if loss_q:
+            loss = loss + (qo * w).sum()
+        if loss_k:
+            loss = loss + (ko * w[:, :2]).sum()
+        loss.backward()
+        return ql.grad if use_q else None, kl.grad if use_k else None
+
+    both = grads(True, True, True, True)
+    assert torch.equal(grads(True, False, True, False)[0], both[0])
+    assert torch.equal(grads(False, True, False, True)[1], both[1])
+    only = grads(True, True, True, False)
+    assert torch.equal(only[0], both[0]) and (only[1] is None or not only[1].any())
+    # the map is linear and orthogonal: <R q, w> = <q, R^T w>
+    lhs = (BL.rope(q, None, tab, pos)[0].double() * w.double()).sum()
+    size = (q.double().abs().sum(-1) * w.double().abs().sum(-1)).sum()
+    assert abs(float(lhs - (q.double() * both[0].double()).sum())) <= 16 * 2.0 ** -24 * float(size)
+    ql = q.clone().requires_grad_(True)
+    p2 = pos.clone()
+    out = BL.rope(ql, None, tab, p2)[0]
+    p2.add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+
+
+def test_gradients_that_start_off_a_16_byte_boundary(BL):
+    """A contiguous slice of a larger gradient (as cat's backward hands out)."""
+    _log("norm_residual: gradient slices")
+    from bit_nf4_quantized_quantize_amd import RopeTable
+    x, h = torch.randn(3, 33, device="cuda"), torch.randn(3, 33, device="cuda").to(torch.bfloat16)
+    w, dy = torch.randn(33, device="cuda"), torch.randn(4, 33, device="cuda")
+
+    def run(cat):
+        xl, hl = x.clone().requires_grad_(True), h.clone().requires_grad_(True)
+        xo, n = BL.norm_residual(xl, hl, w)
+        if cat:
+            (torch.cat([torch.zeros(1, 33, device="cuda"), xo]) * dy).sum().backward(retain_graph=True)
+            torch.cat([n[:1] * 0, n]).backward(dy.to(torch.bfloat16))
+        else:
+            (xo * dy[1:]).sum().backward(retain_graph=True)
+            n.backward(dy[1:].to(torch.bfloat16).clone())
+        return xl.grad, hl.grad
+
+    assert all(torch.equal(a, b) for a, b in zip(run(True), run(False)))
+    tab = RopeTable(2, device="cuda")
+    q, pos = torch.randn(3, 1, 3, device="cuda"), torch.arange(3, device="cuda", dtype=torch.int32)
+    dq = torch.randn(4, 1, 3, device="cuda")
+
+    def turn(cat):
+        ql = q.clone().requires_grad_(True)
+        o = BL.rope(ql, None, tab, pos)[0]
+        torch.cat([torch.zeros(1, 1, 3, device="cuda"), o]).backward(dq) if cat else o.backward(dq[1:].clone())
+        return ql.grad
+
+    assert torch.equal(turn(True), turn(False))
+
+
+def test_cached_calls_check_before_they_touch_the_cache(BL):
+    blk, _, x, _, _ = _setup(BL, 128, 256, 2, 8, 2, 9, 6, 32)
+    for bad in (dict(page_size=8), dict(page_size=48), dict(head_dim=20), dict(head_dim=264)):
+        with pytest.raises(ValueError):
+            BL.PagedCache(**{**dict(num_pages=2, page_size=16, heads=2, head_dim=64, max_seqs=1, max_len=32), **bad})
+    c = blk.cache(8, 16, 2, 32)
+    xc = x.cuda()
+    other = BL.PagedCache(8, 16, 4, 32, 2, 32)
+    for f in (lambda: blk.prefill(xc.double(), c), lambda: blk.prefill(xc[..., :64].contiguous(), c),
+              lambda: blk.prefill(x, c), lambda: blk.decode(xc[:, 0].half(), c), lambda: blk.decode(xc[0], c),
+              lambda: blk.prefill(xc, other), lambda: blk.decode(xc[:, 0], other)):
+        with pytest.raises(ValueError):
+            f()
+    assert c.host_lens == [0, 0] and c.used == 0 and other.used == 0 and c.lens.tolist() == [0, 0]

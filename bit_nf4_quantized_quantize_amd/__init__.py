@@ -32,4 +32,5 @@ from .decoder import (  # noqa: F401
     qlora_paged_plan,
     qlora_rope,
     qlora_rope_cache_write,
+    qlora_rope_frequencies,
 )

@@ -122,9 +122,7 @@ def _new_like(t):
     return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
-def _gain(t, name, shape):
-    if t is not None and (t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape}")
+_F32, _BF16 = (torch.float32,), (torch.bfloat16,)
 
 
 # --------------------------------------------------- norm, gate and residual
@@ -139,7 +137,8 @@ def qlora_norm_residual_fwd(x, h=None, w_pre=None, w_post=None, gate=None, alpha
     given as x itself: the stream is then updated in place."""
     shape, xt = x.shape, x.dtype
     D = shape[-1]
-    _dense(x, "x", shape, _DTYPES)
+    if xt not in _DTYPES or not x.is_contiguous():
+        _dense(x, "x", shape, _DTYPES)
     if h is not None:
         _dense(h, "h", shape, _DTYPES)
         nd = h.dtype
@@ -149,9 +148,9 @@ def qlora_norm_residual_fwd(x, h=None, w_pre=None, w_post=None, gate=None, alpha
         nd = n_dtype if n_dtype is not None else xt
         if nd not in _DTYPES:
             raise ValueError("n_dtype must be torch.float32 or torch.bfloat16")
-    _gain(w_pre, "w_pre", (D,))
-    _gain(w_post, "w_post", (D,))
-    _gain(gate, "gate", (D,))
+    for t, name in ((w_pre, "w_pre"), (w_post, "w_post"), (gate, "gate")):
+        if t is not None:
+            _dense(t, name, (D,), _F32)
     on = _here(stream, x, h, w_pre, w_post, gate, xo, n)
     if on is None:
         with _there(stream, x, h, w_pre, w_post, gate, xo, n):
@@ -203,9 +202,9 @@ def qlora_norm_residual_bwd(dxo, dn, xo, h=None, w_pre=None, w_post=None, gate=N
     for t, name, dt in ((dxo, "dxo", xt), (dx, "dx", xt), (dn, "dn", hd), (h, "h", hd), (dh, "dh", hd)):
         if t is not None:
             _dense(t, name, shape, (dt,))
-    _gain(w_pre, "w_pre", (D,))
-    _gain(w_post, "w_post", (D,))
-    _gain(gate, "gate", (D,))
+    for t, name in ((w_pre, "w_pre"), (w_post, "w_post"), (gate, "gate")):
+        if t is not None:
+            _dense(t, name, (D,), _F32)
     on = _here(stream, xo, dxo, dn, h, w_pre, w_post, gate, dx, dh)
     if on is None:
         with _there(stream, xo, dxo, dn, h, w_pre, w_post, gate, dx, dh):
@@ -330,9 +329,6 @@ def qlora_rope(q, k, table, positions, inverse=False, q_out=None, k_out=None, st
 
 # ------------------------------------------------------ paged key-value cache
 
-_BF16 = (torch.bfloat16,)
-
-
 def _cache(k_cache, v_cache):
     shape = k_cache.shape
     if len(shape) != 4:
@@ -455,7 +451,7 @@ def qlora_paged_attention(q, k_cache, v_cache, block_table, lengths, scale=None,
     else:
         _dense(out, "out", (S, H, d), _BF16)
     if lse is not None:
-        _dense(lse, "lse", (S, H), (torch.float32,))
+        _dense(lse, "lse", (S, H), _F32)
     nws = _attention_workspace(S, H, kvh, d, cols, page)
     ws = q.new_empty(nws // 2) if nws else None  # in q's elements of two bytes
     status = (_lib or lib()).qlora_paged_attention(

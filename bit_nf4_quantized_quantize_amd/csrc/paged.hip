@@ -161,9 +161,9 @@ hipError_t launch_paged_plan(const PlanArgs& a, hipStream_t stream) {
 // it carries 16 bits (one part alone left the outputs 2.2e-3 rel-L2 from the
 // exact ones, two 1.7e-3, the rounding of the output itself; the second product
 // hides under the loads: 280.3 and 280.6 us at 8 sequences of 32768 to 65536, 64
-// on 8 heads).  The sums of the weights are fp32.  The rows of V behind the length are put as
-// zeros into LDS (0 times what lies there would not be 0 for an infinity), the
-// scores there are replaced, not added to.
+// on 8 heads).  The sums of the weights are fp32.  The rows of V behind the
+// length are put as zeros into LDS (0 times what lies there would not be 0 for an
+// infinity), the scores there are replaced, not added to.
 // Measured: 8 sequences of 32768 to 65536 tokens, 64 query heads on 8 kv heads of
 // 128, 282 us (5.7 TB/s; a streaming read reaches 5.6); 16 of 1 to 4096, 32 heads,
 // 102 us (5.3 TB/s); one of 512, 32 heads, 9 us.

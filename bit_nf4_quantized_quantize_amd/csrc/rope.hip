@@ -212,7 +212,8 @@ hipError_t rope_as(const RopeArgs& a, hipStream_t stream) {
   // More than the L2 holds goes past it (8192 tokens of 32 heads to the cache:
   // 79 us against 85; 4096 rotated: 21.9 and 23.5).
   const int64_t bytes = a.T * ((int64_t)a.q_heads + (a.v ? 2 : 1) * a.kv_heads) * a.head_dim * (int64_t)sizeof(T);
-  const auto kernel = bytes > ((int64_t)32 << 20) ? rope_kernel<T, EV, INTER, true, 4> : rope_kernel<T, EV, INTER, false, 4>;
+  const auto kernel =
+      bytes > ((int64_t)32 << 20) ? rope_kernel<T, EV, INTER, true, 4> : rope_kernel<T, EV, INTER, false, 4>;
   const Cuts by = {div_by(units), div_by(hu), div_by(vu), div_by(half ? half : 1)};
   hipLaunchKernelGGL(kernel, dim3((unsigned)gx, gy), dim3(kThreads), lds, stream, a, nt, by);
   return hipGetLastError();

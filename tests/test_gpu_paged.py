@@ -4,9 +4,10 @@ a batch, against the fp64 oracle.
 Tolerance of the attention: a score is a sum of at most 256 exact bfloat16
 products in fp32, so it is off by e = (d + 8) u scale sum |q_i k_i| (u = 2^-24)
 and its weight by a relative e plus 8 u of the exponential and of the score's
-own size; a weight enters the product with V as bfloat16 (half a step, 2^-8)
-and n terms are added, so with W = sum p_i |v_i|
-    |err| <= (2^-8 + 2 e + (n + 256) u) W + 2^-8 |out|,
+own size; a weight enters the product with V as a bfloat16 number and the bfloat16
+remainder (half a step of each, 2^-16) and n terms are added, so with W = sum p_i
+|v_i|
+    |err| <= (2^-16 + 2 e + (n + 256) u) W + 2^-8 |out|,
 the last for the rounding of the output.  The log-sum-exp carries e + (n + 64)
 u and its own rounding."""
 
@@ -65,7 +66,7 @@ def _check(D, q, kc, vc, table, lengths, scale=None):
     qa = np.abs(_n(q)).max(-1)                                         # a score's terms: |q| |k| d at most
     kmax = float(np.abs(_n(kc)[np.isfinite(_n(kc))]).max())
     e = ((d + 8) * U * abs(sc) * (np.abs(_n(q)).sum(-1) * kmax) + 8 * U * abs(sc) * qa * kmax * d)
-    tol = (2.0 ** -8 + 2 * e[..., None] + (n + 256) * U) * wt + 2.0 ** -8 * np.abs(ref)
+    tol = (2.0 ** -16 + 2 * e[..., None] + (n + 256) * U) * wt + 2.0 ** -8 * np.abs(ref)
     err = np.abs(_n(out) - ref)
     assert (err <= tol).all(), (float((err - tol).max()), float(err.max()))
     got = _n(lse)

@@ -15,10 +15,12 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqlora_nf4.so")
+BINDING = os.path.join(PKG, "_decoder.so")  # the CPython module of decoder.py
 
 SOURCES = ["quantize.hip", "linear.hip", "optim.hip", "dropout.hip", "noalloc.hip", "probe.hip", "norm.hip", "rope.hip", "paged.hip",
            "host.cpp", "abi.cpp", "decoder_abi.cpp"]
 HEADERS = ["device.h", "launch.h", "codebooks.h", "decoder.h"]
+# csrc/decoder_binding.cpp is a module of its own, see _build_binding
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -46,8 +48,33 @@ def _compile(src):
     return obj
 
 
+def _build_binding():
+    """Compile the CPython module over the decoder-block ABI (host code against
+    torch's headers) next to the library it links."""
+    import sysconfig
+
+    import torch
+
+    t = os.path.dirname(torch.__file__)
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-isystem", os.path.join(t, "include"),
+           "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"),
+           os.path.join(CSRC, "decoder_binding.cpp"), "-o", tmp,
+           "-L", PKG, "-lqlora_nf4", "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for decoder_binding.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose=True):
-    """Compile every source and link the shared library; returns its path."""
+    """Compile every source and link the shared library and the decoder's
+    module; returns the library's path."""
     os.makedirs(OBJDIR, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(_compile, SOURCES))
@@ -57,6 +84,7 @@ def build(verbose=True):
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _build_binding()
     if verbose:
         print(f"built {LIB}")
     return LIB

@@ -1,7 +1,8 @@
-"""Build libqlora_nf4.so (HIP kernels + C ABI) for gfx950 with hipcc.
+"""Build libqlora_nf4.so (HIP kernels + C ABI) for gfx950 with hipcc, and
+_decoder.so, the Python module of decoder.py, with g++.
 
 Usage: python -m bit_nf4_quantized_quantize_amd.build
-The library is written next to this file; objects go to _build/.
+Both are written next to this file; objects go to _build/.
 """
 
 import concurrent.futures

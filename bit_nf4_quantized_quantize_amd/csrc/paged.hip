@@ -166,7 +166,9 @@ hipError_t launch_paged_plan(const PlanArgs& a, hipStream_t stream) {
 // infinity), the scores there are replaced, not added to.
 // Measured: 8 sequences of 32768 to 65536 tokens, 64 query heads on 8 kv heads of
 // 128, 282 us (5.7 TB/s; a streaming read reaches 5.6); 16 of 1 to 4096, 32 heads,
-// 102 us (5.3 TB/s); one of 512, 32 heads, 9 us.
+// 102 us (5.3 TB/s); one of 512, 32 heads, 9 us, at what 32 CUs read: eight waves
+// take as long, two workgroups per head with half of V's columns each 0.5 us less,
+// but 1 us more at 128 heads.
 
 namespace {
 
@@ -481,7 +483,7 @@ static int64_t groups_of(int64_t S, int q_heads, int kv_heads) {
 }
 
 // No split up to 512 tokens, where one launch takes less than two (1 sequence
-// of 512, 32 heads: 9.5 us against 14); else enough workgroups for four per CU,
+// of 512, 32 heads: 9.5 us against 10.9; 16 of 384: 18.5 and 25); else enough workgroups for four per CU,
 // which evens out sequences of different lengths, or two for less than four
 // sequences (1 of 131072, 32 on 8 heads: 105 us with four, 100 with two), as far
 // as the length gives each wave its tiles.

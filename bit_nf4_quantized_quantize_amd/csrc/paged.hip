@@ -157,11 +157,13 @@ hipError_t launch_paged_plan(const PlanArgs& a, hipStream_t stream) {
 //     tokens in the order in which the scores' lanes hold them, so P goes from
 //     the exponentials into the operand without leaving its lane; V^T comes
 //     from a [token][d] tile in LDS by transposed reads.
-// A weight enters the product as two bfloat16 parts, rounded and remainder, so
-// it carries 16 bits (one part alone left the outputs 2.2e-3 rel-L2 from the
-// exact ones, two 1.7e-3, the rounding of the output itself; the second product
-// hides under the loads: 280.3 and 280.6 us at 8 sequences of 32768 to 65536, 64
-// on 8 heads).  The sums of the weights are fp32.  The rows of V behind the
+// A weight enters the product as three bfloat16 parts, rounded, rounded
+// remainder and the rest, which is exact, so it carries all of its 24 bits: of
+// 65536 outputs 26 are not the rounding of the exact value (8 sequences of 32768
+// to 65536, 64 heads on 8), where fp32 products in a serial sum leave 133.  The
+// two extra products hide under the loads: with two parts and three 289.8 and
+// 289.4 us there, 49.6 and 49.9 for 10 of 5165, 9.7 and 10.0 for one of 512.
+// The sums of the weights are fp32.  The rows of V behind the
 // length are put as zeros into LDS (0 times what lies there would not be 0 for an
 // infinity), the scores there are replaced, not added to.
 // Measured: 8 sequences of 32768 to 65536 tokens, 64 query heads on 8 kv heads of
@@ -212,6 +214,14 @@ __device__ __forceinline__ Pages pages_at(const AttnArgs& a, const int32_t* tabl
 __device__ __forceinline__ void lds_in_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
+}
+
+// The nearest bfloat16 numbers to p; what they leave of p stays there.
+__device__ __forceinline__ bf16x8 take_bf16(float (&p)[8]) {
+  const uint32_t w[4] = {pack_bf2(p[0], p[1]), pack_bf2(p[2], p[3]), pack_bf2(p[4], p[5]), pack_bf2(p[6], p[7])};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) p[j] -= __uint_as_float((j & 1) ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
+  return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
 }
 
 // What the lanes of a wave hold of one tile.
@@ -355,21 +365,16 @@ __global__ __launch_bounds__(64 * W) void paged_attention_kernel(AttnArgs a, int
       p[j] = __builtin_amdgcn_exp2f(p[j] - mu);
       l += p[j];
     }
-    const uint4 pw = make_uint4(pack_bf2(p[0], p[1]), pack_bf2(p[2], p[3]), pack_bf2(p[4], p[5]), pack_bf2(p[6], p[7]));
-    const bf16x8 pb = __builtin_bit_cast(bf16x8, pw);
-    const uint32_t hi[4] = {pw.x, pw.y, pw.z, pw.w};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) p[j] -= __uint_as_float((j & 1) ? hi[j >> 1] & 0xFFFF0000u : hi[j >> 1] << 16);
-    const uint4 rw = make_uint4(pack_bf2(p[0], p[1]), pack_bf2(p[2], p[3]), pack_bf2(p[4], p[5]), pack_bf2(p[6], p[7]));
-    const bf16x8 rb = __builtin_bit_cast(bf16x8, rw);
+    const bf16x8 p1 = take_bf16(p), p2 = take_bf16(p), p3 = take_bf16(p);
     lds_in_order();
 #pragma unroll
     for (int i = 0; i < DP / 16; ++i) {
       const __bf16* src = vt + (4 * g + (col >> 2)) * PITCH + 16 * i + 4 * (col & 3);
       const short4_t v0 = ds_read_tr16(src), v1 = ds_read_tr16(src + 16 * PITCH);
       const short8_t v = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
-      acc[i] = mfma16(__builtin_bit_cast(bf16x8, v), pb, acc[i]);
-      acc[i] = mfma16(__builtin_bit_cast(bf16x8, v), rb, acc[i]);
+      acc[i] = mfma16(__builtin_bit_cast(bf16x8, v), p1, acc[i]);
+      acc[i] = mfma16(__builtin_bit_cast(bf16x8, v), p2, acc[i]);
+      acc[i] = mfma16(__builtin_bit_cast(bf16x8, v), p3, acc[i]);
     }
   }
 

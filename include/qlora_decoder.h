@@ -221,9 +221,9 @@ int qlora_paged_plan(const int32_t* cached_lens, const int32_t* new_lens, int64_
  *   ws        workspace of at least qlora_paged_attention_workspace bytes (may
  *             be 0: ws may then be NULL).
  * Long sequences are split over workgroups and joined by a second kernel in a
- * fixed order; scores, weights' sums and outputs are fp32, a weight enters the
- * product with V as the sum of two bf16 numbers (16 bits).  Results repeat bit
- * for bit.
+ * fixed order; scores, weights, their sums and the products with V are fp32 (a
+ * weight enters as the sum of three bf16 numbers), the output is rounded once.
+ * Results repeat bit for bit.
  */
 int qlora_paged_attention_workspace(int64_t S, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                     int64_t table_cols, int32_t page_size, int64_t* ws_bytes);

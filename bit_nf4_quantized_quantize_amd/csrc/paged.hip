@@ -157,12 +157,13 @@ hipError_t launch_paged_plan(const PlanArgs& a, hipStream_t stream) {
 //     tokens in the order in which the scores' lanes hold them, so P goes from
 //     the exponentials into the operand without leaving its lane; V^T comes
 //     from a [token][d] tile in LDS by transposed reads.
-// A weight enters the product as three bfloat16 parts, rounded, rounded
-// remainder and the rest, which is exact, so it carries all of its 24 bits: of
+// A weight enters the product as three bfloat16 parts whose sum it is, with all
+// of its 24 bits, and which are all positive, so an infinity of V stays one: of
 // 65536 outputs 26 are not the rounding of the exact value (8 sequences of 32768
 // to 65536, 64 heads on 8), where fp32 products in a serial sum leave 133.  The
-// two extra products hide under the loads: with two parts and three 289.8 and
-// 289.4 us there, 49.6 and 49.9 for 10 of 5165, 9.7 and 10.0 for one of 512.
+// products of the remainders hide under the loads: with 16 bits of a weight and
+// with all 290.3 and 290.6 us there, 49.8 and 49.9 for 10 of 5165, 9.7 and 10.2
+// for one of 512.
 // The sums of the weights are fp32.  The rows of V behind the
 // length are put as zeros into LDS (0 times what lies there would not be 0 for an
 // infinity), the scores there are replaced, not added to.
@@ -216,12 +217,37 @@ __device__ __forceinline__ void lds_in_order() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// The nearest bfloat16 numbers to p; what they leave of p stays there.
-__device__ __forceinline__ bf16x8 take_bf16(float (&p)[8]) {
-  const uint32_t w[4] = {pack_bf2(p[0], p[1]), pack_bf2(p[2], p[3]), pack_bf2(p[4], p[5]), pack_bf2(p[6], p[7])};
+// The upper halves of eight words: bfloat16 numbers, where the lower ones are 0.
+__device__ __forceinline__ bf16x8 upper(const uint32_t (&w)[8]) {
+  uint4 v;
+  v.x = __builtin_amdgcn_perm(w[1], w[0], 0x07060302u);
+  v.y = __builtin_amdgcn_perm(w[3], w[2], 0x07060302u);
+  v.z = __builtin_amdgcn_perm(w[5], w[4], 0x07060302u);
+  v.w = __builtin_amdgcn_perm(w[7], w[6], 0x07060302u);
+  return __builtin_bit_cast(bf16x8, v);
+}
+// Weights p as sums of three bfloat16 numbers each, exactly.  A part is the
+// bfloat16 number next below what is left, so a remainder is never zero: 16 bits
+// at most are left after the first and 8 after the second, or the one bit that
+// was between neighbours.  All parts are positive (zero for a weight of zero), so
+// an infinity of V stays what it is in all three products.
+__device__ __forceinline__ void split(const float (&p)[8], bf16x8 (&part)[3]) {
+  uint32_t w[8];
+  float left[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) p[j] -= __uint_as_float((j & 1) ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
-  return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
+  for (int j = 0; j < 8; ++j) left[j] = p[j];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      w[j] = __builtin_elementwise_sub_sat(__float_as_uint(left[j]), 1u) & 0xFFFF0000u;
+      left[j] -= __uint_as_float(w[j]);
+    }
+    part[k] = upper(w);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(left[j]);
+  part[2] = upper(w);
 }
 
 // What the lanes of a wave hold of one tile.
@@ -365,16 +391,16 @@ __global__ __launch_bounds__(64 * W) void paged_attention_kernel(AttnArgs a, int
       p[j] = __builtin_amdgcn_exp2f(p[j] - mu);
       l += p[j];
     }
-    const bf16x8 p1 = take_bf16(p), p2 = take_bf16(p), p3 = take_bf16(p);
+    bf16x8 part[3];
+    split(p, part);
     lds_in_order();
 #pragma unroll
     for (int i = 0; i < DP / 16; ++i) {
       const __bf16* src = vt + (4 * g + (col >> 2)) * PITCH + 16 * i + 4 * (col & 3);
       const short4_t v0 = ds_read_tr16(src), v1 = ds_read_tr16(src + 16 * PITCH);
       const short8_t v = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
-      acc[i] = mfma16(__builtin_bit_cast(bf16x8, v), p1, acc[i]);
-      acc[i] = mfma16(__builtin_bit_cast(bf16x8, v), p2, acc[i]);
-      acc[i] = mfma16(__builtin_bit_cast(bf16x8, v), p3, acc[i]);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) acc[i] = mfma16(__builtin_bit_cast(bf16x8, v), part[k], acc[i]);
     }
   }
 

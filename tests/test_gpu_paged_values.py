@@ -62,3 +62,38 @@ def test_a_weight_enters_the_product_with_all_its_bits(D):
     assert not out[:, 1:].any()
     assert ref.abs().max() > 20 * U            # the case is what it says: bits behind the 16th show
     assert ((out[:, 0] - ref).abs() <= 16 * U / (2 + w) + 2.0 ** -8 * ref.abs()).all()
+
+
+@pytest.mark.parametrize("S,H,KV,d,page,lengths", [
+    (3, 4, 2, 64, 16, [40, 1, 300]), (2, 8, 8, 128, 32, [70, 900]), (1, 34, 2, 80, 16, [1500]), (2, 2, 1, 256, 64, [33, 700])])
+def test_infinities_among_the_attended_values(D, S, H, KV, d, page, lengths):
+    """A column of V with infinities of one sign gives that infinity, with both
+    signs or a NaN gives NaN; the other columns, heads and sequences are, bit for
+    bit, what they were.  The scores are small (|q . k| / sqrt(d) below 10), so no
+    weight is zero."""
+    _log(f"paged attention: infinities S={S} H={H} KV={KV} d={d} lengths={lengths}")
+    g = torch.Generator(device="cuda").manual_seed(d)
+    cols = -(-max(lengths) // page)
+    pages = S * cols
+    q = torch.randn(S, H, d, generator=g, device="cuda").to(BF)
+    kc, vc = (torch.randn(pages, KV, page, d, generator=g, device="cuda").to(BF) for _ in range(2))
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32).view(S, cols)
+    lens = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    lse = torch.empty(S, H, device="cuda")
+    want = D.qlora_paged_attention(q, kc, vc, table, lens, lse=lse).clone()
+    want_lse = lse.clone()
+    inf, nan, G = float("inf"), float("nan"), H // KV
+    for s, n in enumerate(lengths):
+        j = s % KV
+        for c, (at, value) in enumerate([(0, inf), (n - 1, -inf), (n // 2, inf), (n // 3, nan)]):
+            vc[int(table[s, at // page]), j, at % page, 2 * c] = value
+            want[s, j * G:(j + 1) * G, 2 * c] = value
+        if n > 2:
+            vc[int(table[s, (n - 1) // page]), j, (n - 1) % page, 4] = inf    # a second one, of the same sign
+            c = d - 1                                                       # both signs
+            vc[int(table[s, 0]), j, 0, c], vc[int(table[s, 1 // page]), j, 1, c] = inf, -inf
+            want[s, j * G:(j + 1) * G, c] = nan
+    got = D.qlora_paged_attention(q, kc, vc, table, lens, lse=lse)
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got[~got.isnan()], want[~want.isnan()])
+    assert torch.equal(lse, want_lse)

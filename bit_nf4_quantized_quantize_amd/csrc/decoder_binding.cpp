@@ -139,6 +139,13 @@ struct Out {
   const Tensor* get() const { return given ? given : made.defined() ? &made : nullptr; }
 };
 
+// The call has written these tensors of the caller: a backward that saved one
+// of them raises, as after a torch operation in place.
+void wrote(std::initializer_list<const Tensor*> ts) {
+  for (const Tensor* t : ts)
+    if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 // --------------------------------------------- norm, gate and residual
 
 // (x, h, w_pre, w_post, gate, alpha, eps, n_dtype or -1, xo, n) -> (xo, n)
@@ -178,6 +185,7 @@ PyObject* norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                                  as<float>(w_pre), eps, ptr(xo.get()), ptr(n.get()), dev.stream());
   }
   if (st) return PyLong_FromLong(st);
+  wrote({xo.given, n.given});
   return results({xo.get() ? xo.get() : &x, n.get()});
   END_HANDLE_TH_ERRORS
 }
@@ -233,6 +241,7 @@ PyObject* norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                                  made(dw_pre), made(ws), bytes, dev.stream());
   }
   if (st) return PyLong_FromLong(st);
+  wrote({dx.given, dh.given});
   return results({dx.get(), dh.get(), &dw_pre, &dw_post, &dgate});
   END_HANDLE_TH_ERRORS
 }
@@ -288,6 +297,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                     dev.stream());
   }
   if (st) return PyLong_FromLong(st);
+  wrote({q.out.given, k.out.given});
   return results({q.out.get(), k.out.get()});
   END_HANDLE_TH_ERRORS
 }
@@ -334,6 +344,7 @@ PyObject* cache_write(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                                 (const int32_t*)ptr(slots), ptr(kc), ptr(vc), kc.size(0), (int32_t)page, dev.stream());
   }
   if (st) return PyLong_FromLong(st);
+  wrote({&kc, &vc, q.out.given});
   return results({q.out.get()});
   END_HANDLE_TH_ERRORS
 }
@@ -381,6 +392,7 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                           i32(out[0]), i32(out[1]), i32(out[2]), i32(out[3]), i32(out[4]), dev.stream());
   }
   if (st) return PyLong_FromLong(st);
+  wrote({&table, given(0), given(1), given(2), given(3), given(4)});
   return results({&out[0], &out[1], &out[2], &out[3], &out[4]});
   END_HANDLE_TH_ERRORS
 }
@@ -422,6 +434,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                                dev.stream());
   }
   if (st) return PyLong_FromLong(st);
+  wrote({out.given, lse});
   return results({out.get()});
   END_HANDLE_TH_ERRORS
 }

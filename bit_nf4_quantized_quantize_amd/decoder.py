@@ -11,6 +11,11 @@ on one device, which need not be the current one.  Work runs on the current
 stream of that device, or on `stream`; outputs and workspaces a call allocates
 belong to the stream it runs on, and tensors it is given are marked as used
 there, so their memory is not handed out again before the call has run.
+
+These calls are below autograd: results do not require gradients, whatever the
+arguments do (block.norm_residual and block.rope are the differentiable forms).
+A tensor that a call writes into (outputs given, the block table, the caches)
+counts as changed in place, so a backward that saved it raises.
 """
 
 import collections

@@ -289,7 +289,7 @@ class QLoraBlock:
                           self.lin["q"].A.device)
 
     def _check_cached(self, x, cache):
-        """Everything a cached call needs, before the cache is touched."""
+        """What a cached call needs of x, the cache and the rotary table."""
         d = self.hidden // self.heads
         if not self.fused:
             raise ValueError("the cache needs a block in the fused form")
@@ -297,6 +297,20 @@ class QLoraBlock:
             raise ValueError("x must be float32 or bfloat16 and on the cache's device")
         if cache.k.shape[1] != self.heads or cache.k.shape[3] != d:
             raise ValueError(f"the cache must hold {self.heads} heads of {d}")
+        if self.rope is not None and (self.rope.rot_dim > d or self.rope.turns.device != cache.k.device):
+            raise ValueError(f"the rotary table must be of at most {d} elements and on the cache's device")
+
+    def _cached(self, x, cache, new_lens, attend):
+        """_fused on the rows of a plan for new_lens more tokens, attend(plan, q, k,
+        v).  If that fails the cache counts the tokens it had before: what was
+        stored lies behind them and is not used."""
+        before = cache.lens, cache.host_lens, cache.used
+        plan = cache.add(new_lens)
+        try:
+            return self._fused(x, lambda q, k, v: attend(plan, q, k, v))
+        except BaseException:
+            cache.lens, cache.host_lens, cache.used = before
+            raise
 
     @torch.no_grad()
     def prefill(self, x, cache):
@@ -307,16 +321,15 @@ class QLoraBlock:
             raise ValueError(f"prefill needs x [batch, seq, {self.hidden}] and an empty cache of at least batch "
                              "sequences")
         b, t, _ = x.shape
-        plan = cache.add([t if s < b else 0 for s in range(len(cache.host_lens))])
 
-        def attend(q, k, v):
+        def attend(plan, q, k, v):
             if self.rope is not None:
                 q, k = D.qlora_rope(q, k, self.rope, plan.positions)
             D.qlora_rope_cache_write(None, k, v, None, None, plan.slots, cache.k, cache.v)
             q, k, v = (z.float().view(b, t, self.hidden) for z in (q, k, v))
             return causal_attention(q, k, v, self.heads).reshape(b * t, self.hidden).to(torch.bfloat16)
 
-        return self._fused(x, attend)
+        return self._cached(x, cache, [t if s < b else 0 for s in range(len(cache.host_lens))], attend)
 
     @torch.no_grad()
     def decode(self, x, cache):
@@ -326,13 +339,12 @@ class QLoraBlock:
         self._check_cached(x, cache)
         if tuple(x.shape) != (S, self.hidden):
             raise ValueError(f"decode needs x [{S}, {self.hidden}]")
-        plan = cache.add([1] * S)
 
-        def attend(q, k, v):
+        def attend(plan, q, k, v):
             q = D.qlora_rope_cache_write(q, k, v, self.rope, plan.positions, plan.slots, cache.k, cache.v)
             return D.qlora_paged_attention(q, cache.k, cache.v, cache.table, cache.lens).view(S, self.hidden)
 
-        return self._fused(x, attend)
+        return self._cached(x, cache, [1] * S, attend)
 
     def __call__(self, x, checkpoint=False):
         """x: fp32 [batch, seq, hidden] -> y (same shape)."""

@@ -167,12 +167,18 @@ class PagedCache:
     head_dim] of keys and values, the block table, and the pages not in use.
     The lengths are known to the host too, so running out of room raises
     before anything is enqueued.  page_size is a power of two from 16 to 1024,
-    head_dim a multiple of 8 up to 256, as the attention takes them."""
+    head_dim a multiple of 8 up to 256, as the attention takes them, max_seqs at
+    most 4096, as the plan does."""
 
     def __init__(self, num_pages, page_size, heads, head_dim, max_seqs, max_len, device=None):
         dev = device if device is not None else torch.device("cuda", torch.cuda.current_device())
         if page_size not in (16, 32, 64, 128, 256, 512, 1024) or head_dim % 8 or not 8 <= head_dim <= 256:
             raise ValueError("page_size must be a power of two in [16, 1024], head_dim a multiple of 8 in [8, 256]")
+        if not 1 <= max_seqs <= D.PLAN_MAX_SEQS or heads < 1:
+            raise ValueError(f"max_seqs must be in [1, {D.PLAN_MAX_SEQS}], heads at least 1")
+        if not 1 <= num_pages * page_size < 2 ** 31 or not 1 <= max_len <= 2 ** 31 - page_size:
+            raise ValueError("num_pages and max_len must be at least 1, num_pages * page_size and max_len in whole pages "
+                             "below 2^31")
         shape = (num_pages, heads, page_size, head_dim)
         self.k = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
         self.v = torch.zeros(shape, dtype=torch.bfloat16, device=dev)

@@ -269,7 +269,7 @@ class QLoraBlock:
         L, c, T = self.lin, self.residual_scale, x.numel() // self.hidden
         x, n1 = norm_residual(x, None, self.g1)
         n1 = n1.reshape(T, self.hidden)
-        q, k, v = (L[n].bf16(n1).view(T, self.heads, -1) for n in ("q", "k", "v"))
+        q, k, v = (L[n].bf16(n1).view(T, self.heads, self.hidden // self.heads) for n in ("q", "k", "v"))
         o = L["o"].bf16(attend(q, k, v)).view(x.shape)
         h, n2 = norm_residual(x, o, self.g2, self.post1, self.gate1, c)
         n2 = n2.reshape(T, self.hidden)

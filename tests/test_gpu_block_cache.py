@@ -72,3 +72,25 @@ def test_a_wrong_rotary_table_is_named(BL):
     for what in ("more rotated elements than a head has", "a rotary table on the host"):
         with pytest.raises(ValueError, match="rotary table"):
             blocks[what].prefill(x, blocks[what].cache(4, 16, 1, 32))
+
+
+@pytest.mark.parametrize("shape", [(0, 4, HIDDEN), (2, 0, HIDDEN)])
+def test_no_tokens(BL, shape):
+    """As the plain form: an empty result, an empty gradient and zeros for the
+    adapters."""
+    from bit_nf4_quantized_quantize_amd import RopeTable
+    plain = _block(BL)
+    plain.fused = False
+    for blk in (plain, _block(BL), _block(BL, rope=RopeTable(64, device="cuda"),
+                                          post1=torch.ones(HIDDEN, device="cuda", requires_grad=True))):
+        x = torch.randn(*shape, device="cuda", requires_grad=True)
+        y = blk(x)
+        assert y.shape == shape
+        y.sum().backward()
+        assert x.grad.shape == shape
+        assert all(p.grad is not None and not p.grad.any() for p in blk.parameters())
+        if blk.post1 is not None:
+            assert torch.equal(blk.post1.grad, torch.zeros(HIDDEN, device="cuda"))
+        if blk.fused:
+            c = blk.cache(4, 16, 2, 32)
+            assert blk.prefill(x.detach(), c).shape == shape and _state(c) == ([0, 0], [0, 0], 0)

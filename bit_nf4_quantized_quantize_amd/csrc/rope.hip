@@ -5,9 +5,9 @@
 // Bound by HBM: every element is read once and written once.  The angles of a
 // token are the same for all of its heads, so a workgroup first puts the
 // cosines and sines of its NT tokens into LDS (one per token and pair; the
-// angle is position times turns in fp64, less its whole turns, so far
-// positions lose nothing) and then streams the heads of those tokens, 16
-// bytes per thread and access.  Measured: 4096 tokens of 32 + 32 heads of 128
+// angle is position times turns in fp64, less its whole turns, so far positions
+// lose nothing beside the rounding of the table) and then streams the heads of
+// those tokens, 16 bytes per thread and access.  Measured: 4096 tokens of 32 + 32 heads of 128
 // in bfloat16 21 us (6.3 TB/s, part of the output staying in the Infinity
 // Cache), 8191 tokens of 64 + 8 heads in fp32 104 us (5.8 TB/s), 8192 tokens of
 // 32 heads into the cache 78 us (5.2 TB/s), 16 tokens 3.4 us.
@@ -53,11 +53,14 @@ __device__ __forceinline__ void st(T* p, const Piece<T, EV>& v) {
   }
 }
 
-// cos and sin of 2 pi pos turns, times mscale.  The remainder that fp32 drops
-// from the reduced angle is put back to first order.
+// cos and sin of 2 pi pos turns, times mscale.  The product is off by up to half
+// an fp64 step of the whole turns (3 u = 3 * 2^-24 radians at 2^31 positions of
+// 1 radian), so its remainder is put back once those are off; then the angle is
+// exact to 2^-53 turns.  What fp32 drops of it is put back to first order.
 __device__ __forceinline__ void angle(int32_t pos, double turns, float mscale, bool inverse, float* c, float* s) {
   double x = (double)pos * turns;
-  x -= rint(x);
+  const double rest = fma((double)pos, turns, -x);
+  x = (x - rint(x)) + rest;
   if (inverse) x = -x;
   const float f = (float)x;
   const float d = 6.2831853071795865f * (float)(x - (double)f);

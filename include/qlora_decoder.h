@@ -128,7 +128,8 @@ int qlora_rope_frequencies(int32_t rot_dim, double base, int32_t scaling, double
  *             1: a_i = element 2i, b_i = element 2i + 1.
  *   1 <= head_dim <= 1024; rot_dim even, 0 <= rot_dim <= head_dim; strides at
  *   least heads * head_dim; T < 2^24.
- * The angle is reduced in fp64, the rotation is fp32, rounded once.
+ * The angle, its cosine and its sine are fp64; they and mscale's product are
+ * rounded to fp32 once, the rotation is fp32, rounded once.
  */
 int qlora_rope(const void* q, int64_t q_stride, int32_t q_heads, void* qo, int64_t qo_stride, const void* k,
                int64_t k_stride, int32_t kv_heads, void* ko, int64_t ko_stride, int64_t T, int32_t head_dim,

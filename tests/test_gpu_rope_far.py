@@ -68,3 +68,24 @@ def test_far_angles_into_the_cache(D):
     ref = np.array([[_trig(p, t) for t in tab.turns.tolist()] for p in FAR]).reshape(T, rot)
     err = np.abs(kc[0, 0, :T].double().cpu().numpy() - ref)
     assert (err <= (2.0 ** -8 + 8 * U) * np.abs(ref) + 2.0 ** -44).all()
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("scaling", ["none", "yarn"])
+def test_cosines_and_sines_are_rounded_once(D, scaling, inter):
+    """Through q = (1, 0), in float32: the fp64 value times mscale, in one rounding of
+    u of the value at most.  The fp64 functions and product add 2^-50 of it, the
+    angle 2^-52."""
+    print("trig", scaling, inter, flush=True)
+    rot, T = 128, 500
+    tab = D.RopeTable(rot, scaling=scaling, factor=16.0 if scaling == "yarn" else 1.0, original_len=4096,
+                      interleaved=inter, device="cuda")
+    pos = (torch.arange(T, device="cuda") * 777 - 1000).to(torch.int32)
+    q = torch.zeros(T, 1, rot, device="cuda")
+    a, b = (slice(0, rot, 2), slice(1, rot, 2)) if inter else (slice(0, rot // 2), slice(rot // 2, rot))
+    q[..., a] = 1
+    out, _ = D.qlora_rope(q, None, tab, pos)
+    ref = np.array([[_trig(p, t) for t in tab.turns.tolist()] for p in pos.tolist()]) * tab.mscale
+    got = out[:, 0].double().cpu().numpy()
+    for part, want in ((got[:, a], ref[..., 0]), (got[:, b], ref[..., 1])):
+        assert (np.abs(part - want) <= U * (1 + 2.0 ** -20) * np.abs(want) + 2.0 ** -48).all()

@@ -1,5 +1,5 @@
 """Build libqlora_nf4.so (HIP kernels + C ABI) for gfx950 with hipcc, and
-_decoder.so, the Python module of decoder.py, with g++.
+_decoder.so, the Python module of decoder.py (host code, against torch's headers).
 
 Usage: python -m bit_nf4_quantized_quantize_amd.build
 Both are written next to this file; objects go to _build/.
@@ -58,7 +58,7 @@ def _build_binding():
 
     t = os.path.dirname(torch.__file__)
     tmp = BINDING + ".tmp"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+    cmd = [HIPCC, "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", INCLUDE, "-isystem", os.path.join(t, "include"),
            "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"),
@@ -69,7 +69,7 @@ def _build_binding():
            "-L", os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed for decoder_binding.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"hipcc failed for decoder_binding.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
 
 

@@ -34,3 +34,19 @@ def test_the_module_needs_no_other_compiler(tmp_path, monkeypatch):
     r = run([sys.executable, "-c", code], capture_output=True, text=True, env=env, timeout=120)
     assert r.returncode == 0, r.stderr[-2000:]
     assert r.stdout.strip() == str(["attention", "cache_write", "norm_bwd", "norm_fwd", "plan", "rope"])
+
+
+def test_the_build_check_imports_the_module(monkeypatch):
+    """__graft_entry__.build() fails if the module it built does not load."""
+    import __graft_entry__ as entry
+    from bit_nf4_quantized_quantize_amd import decoder
+    if not os.path.exists(build.LIB):
+        pytest.skip("the library is not built")
+    monkeypatch.setattr(build, "build", lambda *a, **k: build.LIB)
+    entry.build()
+    monkeypatch.setattr(decoder, "_native", None)
+    monkeypatch.setitem(sys.modules, "bit_nf4_quantized_quantize_amd._decoder", None)
+    import bit_nf4_quantized_quantize_amd as pkg
+    monkeypatch.delattr(pkg, "_decoder", raising=False)
+    with pytest.raises(decoder.B.QLoraLibraryError):
+        entry.build()

@@ -25,7 +25,10 @@ linears. That form also takes what the plain one lacks: rotary positions
     h = x + c * t1 * post1(L_o(...)),  y = h + c * t2 * post2(L_down(...)),
 gradients for the norm gains and gates that require them, and decoding from
 a paged key-value cache (prefill, decode). The attention core and SiLU stay
-fp32 torch ops.
+fp32 torch ops. Blocks of this form may run on several streams at once and be
+captured into graphs (prefill and decode not: the cache takes counts from the
+host); the plain one shares the binding's workspace of the device, so its calls
+belong on one stream.
 """
 
 import math
@@ -47,23 +50,33 @@ def linear_shapes(hidden, mlp):
             "gate": (mlp, hidden), "up": (mlp, hidden), "down": (hidden, mlp)}
 
 
+class _CallWorkspace:
+    """Scratch of one linear call from the allocator, on the call's stream: calls on
+    other streams and captured graphs share nothing with it, as they would share
+    the binding's own workspace of the device."""
+
+    @staticmethod
+    def get(nbytes, device):
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+
 class _QLoraLinearFn(torch.autograd.Function):
     """Y = X W_bf16^T + s (X A) B on the library's kernels; the backward
     returns dX, dA, dB (no dW)."""
 
     @staticmethod
-    def forward(ctx, X, A, Bm, lin):
-        Y, XA = B.qlora_linear_fwd(X, lin.qw, A, Bm, lin.s)
+    def forward(ctx, X, A, Bm, lin, workspace):
+        Y, XA = B.qlora_linear_fwd(X, lin.qw, A, Bm, lin.s, workspace=workspace)
         ctx.save_for_backward(X, XA, A, Bm)
-        ctx.lin = lin
+        ctx.lin, ctx.workspace = lin, workspace
         return Y
 
     @staticmethod
     def backward(ctx, dY):
         X, XA, A, Bm = ctx.saved_tensors
         lin = ctx.lin
-        dX, dA, dB = B.qlora_linear_bwd(dY.contiguous(), X, XA, lin.qw, A, Bm, lin.s)
-        return dX, dA, dB, None
+        dX, dA, dB = B.qlora_linear_bwd(dY.contiguous(), X, XA, lin.qw, A, Bm, lin.s, workspace=ctx.workspace)
+        return dX, dA, dB, None, None
 
 
 class QLoraLinear:
@@ -81,12 +94,12 @@ class QLoraLinear:
         """z: fp32 [..., in] -> fp32 [..., out] (bf16 at the layer boundary)."""
         lead = z.shape[:-1]
         X = z.reshape(-1, self.in_features).to(torch.bfloat16).contiguous()
-        Y = _QLoraLinearFn.apply(X, self.A, self.B, self)
+        Y = _QLoraLinearFn.apply(X, self.A, self.B, self, None)
         return Y.float().reshape(*lead, self.out_features)
 
     def bf16(self, X):
         """X: bf16 [tokens, in] -> bf16 [tokens, out]."""
-        return _QLoraLinearFn.apply(X.contiguous(), self.A, self.B, self)
+        return _QLoraLinearFn.apply(X.contiguous(), self.A, self.B, self, _CallWorkspace)
 
     def storage_bytes(self):
         return sum(self.qw.sizes.values())

@@ -204,7 +204,8 @@ class PagedCache:
 
     def add(self, new_lens):
         """Room for new_lens[s] more tokens of each sequence: the PagedPlan of
-        their rows, in order of the sequences."""
+        their rows, in order of the sequences. The counts are copied from the host,
+        so a graph cannot hold this call (or prefill and decode, which make it)."""
         if len(new_lens) != len(self.host_lens) or any(n < 0 for n in new_lens):
             raise ValueError(f"new_lens must be {len(self.host_lens)} counts")
         total = [c + n for c, n in zip(self.host_lens, new_lens)]
@@ -214,6 +215,8 @@ class PagedCache:
         need = sum(-(-t // p) - -(-c // p) for t, c in zip(total, self.host_lens))
         if self.used + need > self.free.numel():
             raise ValueError(f"{need} pages needed, {self.free.numel() - self.used} left")
+        if self.lens.is_cuda and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("PagedCache.add cannot be captured into a graph: its counts come from the host")
         new = torch.tensor(new_lens, dtype=torch.int32).to(self.lens.device)
         plan = D.qlora_paged_plan(self.lens, new, self.free[self.used:], self.table, p, sum(new_lens))
         self.lens, self.host_lens, self.used = plan.total_lens, total, self.used + need

@@ -94,3 +94,23 @@ def test_no_tokens(BL, shape):
         if blk.fused:
             c = blk.cache(4, 16, 2, 32)
             assert blk.prefill(x.detach(), c).shape == shape and _state(c) == ([0, 0], [0, 0], 0)
+
+
+def test_cached_calls_are_refused_in_a_capture(BL):
+    """The counts come from the host: a replay could not make them again."""
+    blk = _block(BL)
+    cache = blk.cache(8, 16, 2, 32)
+    x = torch.randn(2, 3, HIDDEN, device="cuda")
+    first = blk.prefill(x, cache)
+    torch.cuda.synchronize()
+    before = _state(cache)
+    graph = torch.cuda.CUDAGraph()
+    row = x[:, 0].contiguous()
+    with torch.cuda.graph(graph):
+        y = row * 2
+        with pytest.raises(RuntimeError, match="captured"):
+            blk.decode(row, cache)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert _state(cache) == before and torch.equal(y, row * 2) and first.isfinite().all()
+    assert blk.decode(row, cache).isfinite().all()

@@ -97,3 +97,29 @@ def test_infinities_among_the_attended_values(D, S, H, KV, d, page, lengths):
     assert torch.equal(got.isnan(), want.isnan())
     assert torch.equal(got[~got.isnan()], want[~want.isnan()])
     assert torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("which", ["q", "k"])
+def test_a_nan_score_spoils_its_own_heads_only(D, which):
+    """A NaN in a query gives that head NaN, one in an attended key the heads of its
+    kv head in its sequence; the rest is, bit for bit, what it was."""
+    _log(f"paged attention: NaN in {which}")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    S, H, KV, d, page, cols = 3, 8, 2, 64, 16, 50
+    q = torch.randn(S, H, d, generator=g, device="cuda").to(BF)
+    kc, vc = (torch.randn(S * cols, KV, page, d, generator=g, device="cuda").to(BF) for _ in range(2))
+    table = torch.randperm(S * cols, generator=g, device="cuda").to(torch.int32).view(S, cols)
+    lens = torch.tensor([700, 5, 33], dtype=torch.int32, device="cuda")
+    lse = torch.empty(S, H, device="cuda")
+    want, want_lse = D.qlora_paged_attention(q, kc, vc, table, lens, lse=lse), lse.clone()
+    spoilt = torch.zeros(S, H, dtype=torch.bool, device="cuda")
+    for s, at in ((0, 650), (2, 0)):
+        if which == "q":
+            q[s, 3, 7] = float("nan")
+            spoilt[s, 3] = True
+        else:
+            kc[int(table[s, at // page]), 1, at % page, 9] = float("nan")
+            spoilt[s, H // KV:] = True
+    got = D.qlora_paged_attention(q, kc, vc, table, lens, lse=lse)
+    assert got[spoilt].isnan().all() and lse[spoilt].isnan().all()
+    assert torch.equal(got[~spoilt], want[~spoilt]) and torch.equal(lse[~spoilt], want_lse[~spoilt])

@@ -5,10 +5,14 @@
 // means in between, bound by HBM: the forward reads x and h and writes xo and
 // n once, the backward reads dxo, xo, dn and h and writes dx and dh once.  A
 // row is held in the registers of its threads (NV chunks of 8 elements each), so
-// nothing is read twice; 512 elements to a wave (1024 beyond 8192).  Measured:
-// 8192 x 8192 in bfloat16 with every part, forward 108-113 us (4.8-4.95 TB/s,
-// a device copy's rate is 4.9), backward 174 us with the sums (4.6 TB/s); 8191 x
-// 4096 with an fp32 stream, backward 127 us (4.75 TB/s).
+// nothing is read twice, but for the backward of rows beyond 8192, which takes
+// them from the caches again; 512 elements to a wave (1024 beyond 8192).
+// Measured: 8192 x 8192 in bfloat16 with every part, forward 108-113 us (4.8-4.95
+// TB/s, a device copy's rate is 4.9), backward 178 us with the sums (4.5 TB/s) and
+// 163 without; 8191 x 4096 with an fp32 stream, backward 127 us (4.75 TB/s) and
+// 120; 4096 x 16384 in bfloat16, backward 233 us (3.5 TB/s).  With few rows the sums
+// set the pace, two rows of partials per workgroup and a second kernel: 256 x 8192
+// in bfloat16 26.5 us with them, 13.8 without.
 #include "decoder.h"
 #include "device.h"
 

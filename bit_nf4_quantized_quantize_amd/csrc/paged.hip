@@ -163,15 +163,15 @@ hipError_t launch_paged_plan(const PlanArgs& a, hipStream_t stream) {
 // to 65536, 64 heads on 8), where fp32 products in a serial sum leave 133.  The
 // products of the remainders hide under the loads: with 16 bits of a weight and
 // with all 290.3 and 290.6 us there, 49.8 and 49.9 for 10 of 5165, 9.7 and 10.2
-// for one of 512.
-// The sums of the weights are fp32.  The rows of V behind the
+// for one of 512.  The sums of the weights are fp32.  The rows of V behind the
 // length are put as zeros into LDS (0 times what lies there would not be 0 for an
 // infinity), the scores there are replaced, not added to.
 // Measured: 8 sequences of 32768 to 65536 tokens, 64 query heads on 8 kv heads of
-// 128, 282 us (5.7 TB/s; a streaming read reaches 5.6); 16 of 1 to 4096, 32 heads,
-// 102 us (5.3 TB/s); one of 512, 32 heads, 9 us, at what 32 CUs read: eight waves
-// take as long, two workgroups per head with half of V's columns each 0.5 us less,
-// but 1 us more at 128 heads.
+// 128, 279-290 us (5.6-5.8 TB/s; a streaming read reaches 5.6); 16 of 1 to 4096, 32
+// heads, 106 us (5.1 TB/s); 8 of 16384 to 32768, 32 heads on 8 kv heads of 256, 274
+// us (5.7 TB/s); one of 512, 32 heads, in a table of 512 9.6-10.2 us, at what 32 CUs
+// read: eight waves take as long, two workgroups per head with half of V's columns
+// each 0.5 us less, but 1 us more at 128 heads.
 
 namespace {
 
@@ -513,11 +513,15 @@ static int64_t groups_of(int64_t S, int q_heads, int kv_heads) {
   return S * kv_heads * ((q_heads / kv_heads + 15) / 16);
 }
 
-// No split up to 512 tokens, where one launch takes less than two (1 sequence
-// of 512, 32 heads: 9.5 us against 10.9; 16 of 384: 18.5 and 25); else enough workgroups for four per CU,
-// which evens out sequences of different lengths, or two for less than four
-// sequences (1 of 131072, 32 on 8 heads: 105 us with four, 100 with two), as far
-// as the length gives each wave its tiles.
+// No split for tables of up to 512 tokens, where one launch takes less than two
+// (1 sequence of 512, 32 heads: 9.5 us against 10.9; 16 of 384: 18.5 and 25); else
+// enough workgroups for four per CU, which evens out sequences of different
+// lengths as far as it cuts them, or two for less than four sequences (1 of 131072,
+// 32 on 8 heads: 105 us with four, 100 with two), as far as the table gives each
+// wave its tiles.  The rule knows the table, not the lengths: one of 512 tokens
+// takes 13.8 us in a table of 4096; and 1024 groups or more are not cut at all, so
+// one long sequence among them sets the time (one of 65536 and 31 of 256, 32 kv
+// heads: 714 us, where the bytes take 215).
 int paged_splits(int64_t S, int q_heads, int kv_heads, int head_dim, int64_t max_len) {
   if (S == 0 || max_len <= 512) return 1;
   const int64_t groups = groups_of(S, q_heads, kv_heads), waves = waves_for(groups, head_dim, max_len);

@@ -42,7 +42,8 @@ extern "C" {
  *   x_dtype, h_dtype      F32 and F32, F32 and BF16, or BF16 and BF16.
  *   T >= 0 (0 enqueues nothing); 1 <= D <= QLORA_NORM_MAX_WIDTH; eps >= 0.
  * fp32 throughout, each output rounded once (n is formed from xo before it is
- * rounded).  xo or n must be given.
+ * rounded).  xo or n must be given.  A row whose sum of squares passes fp32's range
+ * (values beyond 10^17) counts as one of infinite rms.
  */
 int qlora_norm_residual_fwd(const void* x, int32_t x_dtype, const void* h, int32_t h_dtype, int64_t T, int64_t D,
                             const float* w_post, const float* gate, float alpha, const float* w_pre, float eps,

@@ -25,10 +25,10 @@ linears. That form also takes what the plain one lacks: rotary positions
     h = x + c * t1 * post1(L_o(...)),  y = h + c * t2 * post2(L_down(...)),
 gradients for the norm gains and gates that require them, and decoding from
 a paged key-value cache (prefill, decode). The attention core and SiLU stay
-fp32 torch ops. Blocks of this form may run on several streams at once and be
-captured into graphs (prefill and decode not: the cache takes counts from the
-host); the plain one shares the binding's workspace of the device, so its calls
-belong on one stream.
+fp32 torch ops. Blocks of this form may run on several streams at once, and
+their forward be captured into a graph (prefill and decode not: the cache takes
+counts from the host); the plain one shares the binding's workspace of the
+device, so its calls belong on one stream.
 """
 
 import math
@@ -51,9 +51,9 @@ def linear_shapes(hidden, mlp):
 
 
 class _CallWorkspace:
-    """Scratch of one linear call from the allocator, on the call's stream: calls on
-    other streams and captured graphs share nothing with it, as they would share
-    the binding's own workspace of the device."""
+    """Scratch of one linear call from the allocator, on the call's stream. The
+    binding's own is one per device: calls on other streams and captured graphs
+    would share it."""
 
     @staticmethod
     def get(nbytes, device):

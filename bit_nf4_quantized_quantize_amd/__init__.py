@@ -4,7 +4,8 @@ NF4 blockwise quantisation with double quantisation, dequantisation, and the
 forward/backward of a linear layer with a LoRA adapter over the frozen NF4
 weight, as hand-written HIP kernels behind the C ABI of include/qlora_nf4.h.
 `binding` is the ctypes layer over that ABI; `decoder` the one over
-include/qlora_decoder.h (norms and residual, rotary positions, paged decoding);
+include/qlora_decoder.h (norms and residual, rotary positions, paged decoding),
+`kvcache` that over include/qlora_kvcache.h (8-bit and shared key-value caches);
 `build` compiles the library.
 """
 
@@ -33,4 +34,11 @@ from .decoder import (  # noqa: F401
     qlora_rope,
     qlora_rope_cache_write,
     qlora_rope_frequencies,
+)
+from .kvcache import (  # noqa: F401
+    KVCache,
+    qlora_kv_attention,
+    qlora_kv_read,
+    qlora_kv_write,
+    qlora_prefix_attention,
 )

@@ -1,8 +1,9 @@
 """Build libqlora_nf4.so (HIP kernels + C ABI) for gfx950 with hipcc, and
-_decoder.so, the Python module of decoder.py (host code, against torch's headers).
+_decoder.so and _kvcache.so, the Python modules of decoder.py and kvcache.py
+(host code, against torch's headers).
 
 Usage: python -m bit_nf4_quantized_quantize_amd.build
-Both are written next to this file; objects go to _build/.
+All are written next to this file; objects go to _build/.
 """
 
 import concurrent.futures
@@ -17,11 +18,12 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqlora_nf4.so")
 BINDING = os.path.join(PKG, "_decoder.so")  # the CPython module of decoder.py
+KV_BINDING = os.path.join(PKG, "_kvcache.so")  # that of kvcache.py
 
 SOURCES = ["quantize.hip", "linear.hip", "optim.hip", "dropout.hip", "noalloc.hip", "probe.hip", "norm.hip", "rope.hip", "paged.hip",
-           "host.cpp", "abi.cpp", "decoder_abi.cpp"]
-HEADERS = ["device.h", "launch.h", "codebooks.h", "decoder.h"]
-# csrc/decoder_binding.cpp is a module of its own, see _build_binding
+           "kv_write.hip", "kv_attention.hip", "host.cpp", "abi.cpp", "decoder_abi.cpp", "kv_abi.cpp"]
+HEADERS = ["device.h", "launch.h", "codebooks.h", "decoder.h", "rotary.h", "paged_device.h", "kvcache.h", "abi_checks.h"]
+# csrc/decoder_binding.cpp and kv_binding.cpp are modules of their own, see _build_module
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -49,33 +51,37 @@ def _compile(src):
     return obj
 
 
-def _build_binding():
-    """Compile the CPython module over the decoder-block ABI (host code against
-    torch's headers) next to the library it links."""
+def _build_module(source, out):
+    """Compile a CPython module over the ABI (host code against torch's headers)
+    next to the library it links."""
     import sysconfig
 
     import torch
 
     t = os.path.dirname(torch.__file__)
-    tmp = BINDING + ".tmp"
+    tmp = out + ".tmp"
     cmd = [HIPCC, "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", INCLUDE, "-isystem", os.path.join(t, "include"),
            "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"],
            "-isystem", os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"),
-           os.path.join(CSRC, "decoder_binding.cpp"), "-o", tmp,
+           os.path.join(CSRC, source), "-o", tmp,
            "-L", PKG, "-lqlora_nf4", "-Wl,-rpath,$ORIGIN",
            "-L", os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"hipcc failed for decoder_binding.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
+        raise RuntimeError(f"hipcc failed for {source}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
+
+
+def _build_binding():
+    _build_module("decoder_binding.cpp", BINDING)
 
 
 def build(verbose=True):
-    """Compile every source and link the shared library and the decoder's
-    module; returns the library's path."""
+    """Compile every source and link the shared library and the Python modules;
+    returns the library's path."""
     os.makedirs(OBJDIR, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(_compile, SOURCES))
@@ -85,7 +91,9 @@ def build(verbose=True):
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _build_binding()
+    with concurrent.futures.ThreadPoolExecutor(max_workers=2) as ex:
+        for f in [ex.submit(_build_binding), ex.submit(_build_module, "kv_binding.cpp", KV_BINDING)]:
+            f.result()
     if verbose:
         print(f"built {LIB}")
     return LIB

@@ -1,0 +1,440 @@
+// Attention of one new token per sequence over a paged cache of any type, and
+// over a prefix that the sequences share, gfx950 (definitions in
+// include/qlora_kvcache.h).
+#include <type_traits>
+
+#include "device.h"
+#include "kvcache.h"
+#include "paged_device.h"
+
+namespace qlora {
+
+// ------------------------------------------------- few rows: narrow workgroups
+
+namespace {
+
+template <int CT>
+constexpr bool kCoded = CT != kCacheBf16;
+
+__device__ __forceinline__ int64_t cut_length(int64_t n, int64_t cols, int shift) {
+  const int64_t cap = cols << shift;
+  return n < 0 ? 0 : n > cap ? cap : n;
+}
+
+// Eight codes as bfloat16 numbers, exactly.
+template <int CT>
+__device__ __forceinline__ uint4 numbers(uint32_t lo, uint32_t hi) {
+  uint32_t w[4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t c = h ? hi : lo;
+    if constexpr (CT == kCacheE4m3) {
+      w[2 * h] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false));
+      w[2 * h + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true));
+    } else {
+      // whole numbers of 8 bits: the upper half of their fp32 form holds them
+      float f[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = (float)(int8_t)(c >> (8 * j));
+      w[2 * h] = __builtin_amdgcn_perm(__float_as_uint(f[1]), __float_as_uint(f[0]), 0x07060302u);
+      w[2 * h + 1] = __builtin_amdgcn_perm(__float_as_uint(f[3]), __float_as_uint(f[2]), 0x07060302u);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The pages of the two halves of a tile (-1: none, or behind the length).
+struct Halves {
+  int32_t of[2];
+};
+__device__ __forceinline__ Halves halves_at(const int32_t* table, int64_t tok, int64_t n, int shift) {
+  Halves p;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) p.of[h] = tok + 16 * h < n ? table[(tok + 16 * h) >> shift] : -1;
+  return p;
+}
+
+// What the lanes of a wave hold of one tile of 32 tokens.
+//   bf16:  k token 16 half + lane % 16, elements 32 i + 8 (lane / 16) ..
+//   codes: the same token, elements 64 i + 16 (lane / 16) .., two steps of the
+//          product in one load; the order of the elements in the reduction is
+//          free as long as Q has the same
+//   v: pieces i * 64 + lane of the 32 rows
+template <int DP, int CT>
+struct KvTile {
+  static constexpr int EV = kCoded<CT> ? 16 : 8;                    // elements in 16 bytes
+  static constexpr int KI = kCoded<CT> ? (DP + 63) / 64 : DP / 32;  // loads of a key per lane
+  static constexpr int STEPS = kCoded<CT> ? 2 * KI : KI;            // of 32 elements
+  static constexpr int VI = kTile * DP / EV / 64;
+  uint4 k[2][KI];
+  uint4 v[VI];
+  float4 ks[2], vs[2];  // scales of the tokens 16 half + 4 (lane / 16) ..
+  bool ok[2];           // the halves lie in pages of the cache
+};
+
+template <int DP, int CT>
+__device__ __forceinline__ void load_tile(KvTile<DP, CT>& t, const KvCache& c, const Halves& p, int64_t tok, int kv,
+                                          int lane) {
+  using Tile = KvTile<DP, CT>;
+  typedef typename std::conditional<kCoded<CT>, uint8_t, uint16_t>::type Elem;
+  constexpr int CH = DP / Tile::EV;
+  const int d = c.head_dim;
+  int64_t row[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int32_t page = __builtin_amdgcn_readfirstlane(p.of[h]);
+    t.ok[h] = page >= 0 && page < c.num_pages;
+    // without a page the loads go to the cache's first rows and count nothing
+    const int64_t first = (tok + 16 * h) & ((1 << c.page_shift) - 1);
+    row[h] = t.ok[h] ? (((int64_t)page * c.kv_heads + kv) << c.page_shift) + first : 0;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const Elem* key = (const Elem*)c.k + (row[h] + (lane & 15)) * d;
+#pragma unroll
+    for (int i = 0; i < Tile::KI; ++i) {
+      const int e = (4 * i + (lane >> 4)) * Tile::EV;
+      t.k[h][i] = *reinterpret_cast<const uint4*>(key + (e < d ? e : 0));
+    }
+    if constexpr (kCoded<CT>) {
+      t.ks[h] = *reinterpret_cast<const float4*>(c.k_scale + row[h] + 4 * (lane >> 4));
+      t.vs[h] = *reinterpret_cast<const float4*>(c.v_scale + row[h] + 4 * (lane >> 4));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < Tile::VI; ++i) {
+    const int idx = i * 64 + lane, r = idx / CH, e = idx % CH * Tile::EV;
+    t.v[i] = *reinterpret_cast<const uint4*>((const Elem*)c.v + ((r < 16 ? row[0] : row[1]) + (r & 15)) * d +
+                                             (e < d ? e : 0));
+  }
+}
+
+__device__ __forceinline__ float part_of(const float4& v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
+
+// The query rows of a workgroup are the 16 columns of its products: heads that
+// share a kv head, of one sequence or, over the prefix, of any.
+struct Columns {
+  int64_t s;    // sequence, or -1: rows of all of them from r0
+  int64_t r0;   // first row (sequence * group + head of the group), or head
+  int n, group, kv;
+};
+__device__ __forceinline__ void place_of(const Columns& c, int col, int64_t* s, int* head) {
+  const int64_t r = c.r0 + col;
+  if (c.s >= 0) {
+    *s = c.s, *head = c.kv * c.group + (int)r;
+  } else {
+    *s = r / c.group, *head = c.kv * c.group + (int)(r % c.group);
+  }
+}
+
+// Grid: y < ptiles are the prefix's tiles of 16 rows, then the sequences; x: kv
+// heads, tiles of heads and parts.
+template <int DP, int W, int CT>
+__global__ __launch_bounds__(64 * W) void kv_attention_kernel(KvAttnArgs a, int qtiles, int ptiles) {
+  using Tile = KvTile<DP, CT>;
+  constexpr int CH = DP / Tile::EV;
+  constexpr int PITCH = DP + 16;  // of the V tile: 16 rows of one column go to different banks
+  constexpr int OP = DP + 4;      // of the partial outputs
+  constexpr int WAVE_BYTES = kTile * PITCH * 2;
+  static_assert(16 * OP * 4 <= WAVE_BYTES, "a wave's outputs take the place of its V tile");
+  __shared__ __attribute__((aligned(16))) char lds[W * WAVE_BYTES];
+  __shared__ float s_m[W][16], s_l[W][16];
+
+  const KvCache& kc = a.c;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, col = lane & 15, d = kc.head_dim;
+  const int group = a.q_heads / kc.kv_heads, parts = a.psplits + a.splits;
+  const bool shared = (int)blockIdx.y < ptiles;
+  Columns cols;
+  cols.group = group;
+  int id = blockIdx.x, z;
+  int64_t n;
+  const int32_t* table;
+  Cut cut;
+  if (shared) {
+    if (id >= kc.kv_heads * a.psplits) return;
+    z = id % a.psplits;
+    cols.kv = id / a.psplits;
+    cols.s = -1, cols.r0 = (int64_t)blockIdx.y * 16;
+    const int64_t left = a.S * group - cols.r0;
+    cols.n = left < 16 ? (int)left : 16;
+    n = cut_length(*a.prefix_len, a.prefix_cols, kc.page_shift);
+    table = a.prefix_table;
+    cut = cut_of(n, a.psplits, W);
+  } else {
+    if (id >= kc.kv_heads * qtiles * a.splits) return;
+    z = id % a.splits;
+    id /= a.splits;
+    const int qt = id % qtiles;
+    cols.kv = id / qtiles;
+    cols.s = blockIdx.y - ptiles, cols.r0 = qt * 16;
+    cols.n = group - qt * 16 < 16 ? group - qt * 16 : 16;
+    n = cut_length(a.lengths[cols.s], a.table_cols, kc.page_shift);
+    table = a.table + cols.s * a.table_cols;
+    cut = cut_of(n, a.splits, W);
+  }
+  if (parts > 1 && z >= cut.parts) return;
+  const int64_t first = z * cut.per;
+  const int64_t last = first + cut.per < cut.tiles ? first + cut.per : cut.tiles;
+
+  // Q^T: column col (a query row), reduction elements as the keys' lanes hold them
+  bf16x8 q[Tile::STEPS];
+  {
+    int64_t s = 0;
+    int head = 0;
+    if (col < cols.n) place_of(cols, col, &s, &head);
+    const uint16_t* src = a.q + s * a.q_stride + (int64_t)head * d;
+#pragma unroll
+    for (int i = 0; i < Tile::STEPS; ++i) {
+      const int e = kCoded<CT> ? 64 * (i / 2) + 16 * g + 8 * (i % 2) : 32 * i + 8 * g;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (col < cols.n && e < d) v = *reinterpret_cast<const uint4*>(src + e);
+      q[i] = __builtin_bit_cast(bf16x8, v);
+    }
+  }
+  const float scale2 = a.scale * 1.44269504088896340736f;  // scores in base 2
+  float m = -INFINITY, l = 0.0f;
+  floatx4 acc[DP / 16];
+#pragma unroll
+  for (int t = 0; t < DP / 16; ++t) acc[t] = (floatx4){0, 0, 0, 0};
+  __bf16* vt = reinterpret_cast<__bf16*>(lds + wave * WAVE_BYTES);
+
+  // the loads of the next tile run under the products of this one, and the
+  // look-up of the pages after that, so neither waits for the other
+  Tile t;
+  int64_t ti = first + wave;
+  Halves pages = halves_at(table, ti * kTile, n, kc.page_shift);
+  if (ti < last) load_tile<DP, CT>(t, kc, pages, ti * kTile, cols.kv, lane);
+  pages = halves_at(table, (ti + W) * kTile, n, kc.page_shift);
+  for (; ti < last; ti += W) {
+    const int64_t tok = ti * kTile;
+    const bool full = tok + kTile <= n && t.ok[0] && t.ok[1];
+    // V to LDS
+    lds_in_order();
+#pragma unroll
+    for (int i = 0; i < Tile::VI; ++i) {
+      const int idx = i * 64 + lane, r = idx / CH, e = idx % CH * Tile::EV;
+      uint4 v = t.v[i];
+      if (!full && !(tok + r < n && (r < 16 ? t.ok[0] : t.ok[1]))) v = make_uint4(0, 0, 0, 0);
+      uint4* dst = reinterpret_cast<uint4*>(vt + r * PITCH + e);
+      if constexpr (kCoded<CT>) {
+        dst[0] = numbers<CT>(v.x, v.y);
+        dst[1] = numbers<CT>(v.z, v.w);
+      } else {
+        dst[0] = v;
+      }
+    }
+    // scores
+    floatx4 sc[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      sc[h] = (floatx4){0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < Tile::KI; ++i) {
+        uint4 k = t.k[h][i];
+        if (d < 4 * Tile::KI * Tile::EV && (4 * i + g) * Tile::EV >= d) k = make_uint4(0, 0, 0, 0);
+        if constexpr (kCoded<CT>) {
+          sc[h] = mfma16(__builtin_bit_cast(bf16x8, numbers<CT>(k.x, k.y)), q[2 * i], sc[h]);
+          sc[h] = mfma16(__builtin_bit_cast(bf16x8, numbers<CT>(k.z, k.w)), q[2 * i + 1], sc[h]);
+        } else {
+          sc[h] = mfma16(__builtin_bit_cast(bf16x8, k), q[i], sc[h]);
+        }
+      }
+    }
+    const bool ok0 = t.ok[0], ok1 = t.ok[1];
+    float p[8], vs[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      p[j] = sc[j >> 2][j & 3] * (kCoded<CT> ? part_of(t.ks[j >> 2], j & 3) * scale2 : scale2);
+      vs[j] = kCoded<CT> ? part_of(t.vs[j >> 2], j & 3) : 1.0f;
+    }
+    if (ti + W < last) load_tile<DP, CT>(t, kc, pages, tok + W * kTile, cols.kv, lane);
+    pages = halves_at(table, tok + 2 * W * kTile, n, kc.page_shift);
+    if (!full) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (!(tok + 16 * (j >> 2) + 4 * g + (j & 3) < n && (j < 4 ? ok0 : ok1))) p[j] = -INFINITY, vs[j] = 0.0f;
+    }
+    float mt = m;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mt = fmaxf(mt, p[j]);
+    mt = fmaxf(mt, __shfl_xor(mt, 16, 64));
+    mt = fmaxf(mt, __shfl_xor(mt, 32, 64));
+    const float mu = mt == -INFINITY ? 0.0f : mt;
+    if (__ballot(mt > m)) {
+      const float old = __builtin_amdgcn_exp2f(m - mu);
+      l *= old;
+#pragma unroll
+      for (int i = 0; i < DP / 16; ++i) acc[i] *= old;
+    }
+    m = mt;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      p[j] = __builtin_amdgcn_exp2f(p[j] - mu);
+      l += p[j];
+      if constexpr (kCoded<CT>) p[j] *= vs[j];
+    }
+    bf16x8 part[3];
+    split(p, part);
+    lds_in_order();
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i) {
+      const __bf16* src = vt + (4 * g + (col >> 2)) * PITCH + 16 * i + 4 * (col & 3);
+      const short4_t v0 = ds_read_tr16(src), v1 = ds_read_tr16(src + 16 * PITCH);
+      const short8_t v = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) acc[i] = mfma16(__builtin_bit_cast(bf16x8, v), part[k], acc[i]);
+    }
+  }
+
+  // join the waves: each lane group holds the sum of its own tokens
+  l += __shfl_xor(l, 16, 64);
+  l += __shfl_xor(l, 32, 64);
+  if (g == 0) s_m[wave][col] = m, s_l[wave][col] = l;
+  lds_in_order();
+  float* ow = reinterpret_cast<float*>(lds + wave * WAVE_BYTES);
+#pragma unroll
+  for (int i = 0; i < DP / 16; ++i) *reinterpret_cast<floatx4*>(ow + col * OP + 16 * i + 4 * g) = acc[i];
+  __syncthreads();
+  for (int e = threadIdx.x; e < cols.n * (d / 4); e += 64 * W) {
+    const int h = e / (d / 4), c = e % (d / 4) * 4;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_m[w][h]);
+    const float mu = mx == -INFINITY ? 0.0f : mx;
+    float sum = 0.0f;
+    floatx4 o = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float f = __builtin_amdgcn_exp2f(s_m[w][h] - mu);
+      sum += s_l[w][h] * f;
+      o += *reinterpret_cast<const floatx4*>(reinterpret_cast<const float*>(lds + w * WAVE_BYTES) + h * OP + c) * f;
+    }
+    int64_t s;
+    int head;
+    place_of(cols, h, &s, &head);
+    const int64_t row = s * a.q_heads + head;
+    if (parts > 1) {
+      const int64_t at = row * parts + (shared ? z : a.psplits + z);
+      *reinterpret_cast<floatx4*>(a.part_o + at * d + c) = o;
+      if (c == 0) a.part_ml[at * 2] = mx, a.part_ml[at * 2 + 1] = sum;
+    } else {
+      o *= sum == 0.0f ? 0.0f : 1.0f / sum;
+      *reinterpret_cast<uint2*>(a.out + row * d + c) = make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
+      if (a.lse && c == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994530942f;
+    }
+  }
+}
+
+// Joins the parts of a row, one workgroup per sequence and head: its threads
+// hold four elements of the head each and take the parts in turns of 1024 /
+// head_dim, then the turns' sums are added in order.
+constexpr int kMaxParts = 256;
+
+__global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs a) {
+  __shared__ float s_f[kMaxParts], s_m[4], s_l[4];
+  __shared__ floatx4 s_o[256];
+  const int64_t s = blockIdx.y, row = s * a.q_heads + blockIdx.x;
+  const int d = a.c.head_dim, dq = d / 4, t = threadIdx.x, all = a.psplits + a.splits;
+  const int own = (int)cut_of(cut_length(a.lengths[s], a.table_cols, a.c.page_shift), a.splits, a.waves).parts;
+  int pre = 0;
+  if (a.psplits) {
+    const int64_t n = cut_length(*a.prefix_len, a.prefix_cols, a.c.page_shift);
+    pre = (int)cut_of(n, a.psplits, a.pwaves).parts;
+  }
+  // part i of those there are lies at i, behind the prefix's at psplits ..
+  const int parts = pre + own, gap = a.psplits - pre;
+  float m = -INFINITY, l = 0.0f;
+  if (t < parts) {
+    const float2 v = *reinterpret_cast<const float2*>(a.part_ml + (row * all + (t < pre ? t : t + gap)) * 2);
+    m = v.x, l = v.y;
+  }
+  const float wm = wave_max(m);
+  if ((t & 63) == 0) s_m[t >> 6] = wm;
+  __syncthreads();
+  const float mx = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3])), mu = mx == -INFINITY ? 0.0f : mx;
+  const float f = __builtin_amdgcn_exp2f(m - mu);
+  l *= f;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) l += __shfl_xor(l, o, 64);
+  s_f[t] = f;
+  if ((t & 63) == 0) s_l[t >> 6] = l;
+  __syncthreads();
+  const float sum = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]), inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  if (a.lse && t == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994530942f;
+  const int turns = 256 / dq, turn = t / dq, c = t - turn * dq;
+  floatx4 o = {0, 0, 0, 0};
+  if (turn < turns) {
+    const float* src = a.part_o + row * all * d + 4 * c;
+#pragma unroll 4
+    for (int z = turn; z < parts; z += turns)
+      o += *reinterpret_cast<const floatx4*>(src + (int64_t)(z < pre ? z : z + gap) * d) * s_f[z];
+  }
+  s_o[t] = o;
+  __syncthreads();
+  if (t < dq) {
+    for (int k = 1; k < turns; ++k) o += s_o[k * dq + t];
+    o *= inv;
+    *reinterpret_cast<uint2*>(a.out + row * d + 4 * t) = make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
+  }
+}
+
+template <int DP, int W, int CT>
+void attention_as(const KvAttnArgs& a, hipStream_t stream) {
+  const int group = a.q_heads / a.c.kv_heads, qtiles = (group + 15) / 16;
+  const int64_t ptiles = a.psplits ? (a.S * group + 15) / 16 : 0;
+  const int own = qtiles * a.splits, wide = own > a.psplits ? own : a.psplits;
+  hipLaunchKernelGGL((kv_attention_kernel<DP, W, CT>), dim3((unsigned)(a.c.kv_heads * wide), (unsigned)(a.S + ptiles)),
+                     dim3(64 * W), 0, stream, a, qtiles, (int)ptiles);
+}
+
+template <int DP, int CT>
+void attention_waves(const KvAttnArgs& a, hipStream_t stream) {
+  if (a.waves == 8) attention_as<DP, 8, CT>(a, stream);
+  else attention_as<DP, 4, CT>(a, stream);
+}
+
+template <int CT>
+void attention_of(const KvAttnArgs& a, hipStream_t stream) {
+  if (a.c.head_dim <= 64) attention_waves<64, CT>(a, stream);
+  else if (a.c.head_dim <= 96) attention_waves<96, CT>(a, stream);
+  else if (a.c.head_dim <= 128) attention_waves<128, CT>(a, stream);
+  else attention_as<256, 4, CT>(a, stream);
+}
+
+int waves_for(int64_t groups, int head_dim, int64_t max_len) {
+  return groups * ((max_len + kTile - 1) / kTile) >= 128 * 256 && head_dim <= 128 ? 8 : 4;
+}
+
+}  // namespace
+
+KvParts kv_parts(const KvCache& c, int64_t S, int q_heads, int64_t table_cols, int64_t prefix_cols) {
+  KvParts p;
+  const int64_t max_len = table_cols << c.page_shift;
+  p.own = paged_splits(S, q_heads, c.kv_heads, c.head_dim, max_len);
+  p.prefix = 0;
+  if (!prefix_cols || !S) return p;
+  const int64_t rows = S * (q_heads / c.kv_heads), groups = c.kv_heads * ((rows + 15) / 16);
+  int64_t n = (2 * 256 + groups - 1) / groups;
+  const int64_t least = 4 * kMinTiles * kTile, most = ((prefix_cols << c.page_shift) + least - 1) / least;
+  if (n > most) n = most;
+  if (n > kMaxParts / 2) n = kMaxParts / 2;
+  p.prefix = n < 1 ? 1 : (int)n;
+  if (p.own > kMaxParts / 2) p.own = kMaxParts / 2;
+  return p;
+}
+
+hipError_t launch_kv_attention(const KvAttnArgs& args, hipStream_t stream) {
+  KvAttnArgs a = args;
+  const int64_t group = a.q_heads / a.c.kv_heads;
+  a.waves = a.psplits ? 4 : waves_for(a.S * a.c.kv_heads * ((group + 15) / 16), a.c.head_dim, a.table_cols << a.c.page_shift);
+  a.pwaves = a.waves;
+  if (a.c.type == kCacheInt8) attention_of<kCacheInt8>(a, stream);
+  else if (a.c.type == kCacheE4m3) attention_of<kCacheE4m3>(a, stream);
+  else attention_of<kCacheBf16>(a, stream);
+  if (a.psplits + a.splits > 1)
+    hipLaunchKernelGGL(kv_join_kernel, dim3(a.q_heads, (unsigned)a.S), dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace qlora

@@ -13,6 +13,7 @@
 // 32 heads into the cache 78 us (5.2 TB/s), 16 tokens 3.4 us.
 #include "decoder.h"
 #include "device.h"
+#include "rotary.h"
 
 namespace qlora {
 
@@ -51,22 +52,6 @@ __device__ __forceinline__ void st(T* p, const Piece<T, EV>& v) {
   } else {
     *reinterpret_cast<Piece<T, EV>*>(p) = v;
   }
-}
-
-// cos and sin of 2 pi pos turns, times mscale.  The product is off by up to half
-// an fp64 step of the whole turns (3 u = 3 * 2^-24 radians at 2^31 positions of
-// 1 radian), so its remainder is put back once those are off; then the angle is
-// exact to 2^-53 turns.  The functions are fp64 too, rounded once: they are few
-// beside the elements (fp32 functions take as long, 104.2 us at 8191 tokens of 72
-// heads, 103.5 with these).
-__device__ __forceinline__ void angle(int32_t pos, double turns, float mscale, bool inverse, float* c, float* s) {
-  double x = (double)pos * turns;
-  const double rest = fma((double)pos, turns, -x);
-  x = (x - rint(x)) + rest;
-  double sn, cs;
-  sincospi(2.0 * x, &sn, &cs);
-  *c = (float)(cs * mscale);
-  *s = (float)((inverse ? -sn : sn) * mscale);
 }
 
 // Where a head's row goes.
@@ -186,7 +171,7 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, int nt, Cuts
   load();
   for (int i = threadIdx.x; i < n * half; i += kThreads) {
     const int tk = i / by.half;
-    angle(a.positions[t0 + tk], a.turns[i - tk * half], a.mscale, a.inverse, cs + i, sn + i);
+    rotary_angle(a.positions[t0 + tk], a.turns[i - tk * half], a.mscale, a.inverse, cs + i, sn + i);
   }
   __syncthreads();
   while (i0 < total) {

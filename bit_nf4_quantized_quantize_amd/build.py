@@ -21,8 +21,9 @@ BINDING = os.path.join(PKG, "_decoder.so")  # the CPython module of decoder.py
 KV_BINDING = os.path.join(PKG, "_kvcache.so")  # that of kvcache.py
 
 SOURCES = ["quantize.hip", "linear.hip", "optim.hip", "dropout.hip", "noalloc.hip", "probe.hip", "norm.hip", "rope.hip", "paged.hip",
-           "kv_write.hip", "kv_attention.hip", "host.cpp", "abi.cpp", "decoder_abi.cpp", "kv_abi.cpp"]
-HEADERS = ["device.h", "launch.h", "codebooks.h", "decoder.h", "rotary.h", "paged_device.h", "kvcache.h", "abi_checks.h"]
+           "kv_write.hip", "kv_attention.hip", "kv_prefix.hip", "host.cpp", "abi.cpp", "decoder_abi.cpp", "kv_abi.cpp"]
+HEADERS = ["device.h", "launch.h", "codebooks.h", "decoder.h", "rotary.h", "paged_device.h", "kvcache.h",
+           "kv_codes.h", "abi_checks.h"]
 # csrc/decoder_binding.cpp and kv_binding.cpp are modules of their own, see _build_module
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -4,6 +4,7 @@
 #include <type_traits>
 
 #include "device.h"
+#include "kv_codes.h"
 #include "kvcache.h"
 #include "paged_device.h"
 
@@ -19,28 +20,6 @@ constexpr bool kCoded = CT != kCacheBf16;
 __device__ __forceinline__ int64_t cut_length(int64_t n, int64_t cols, int shift) {
   const int64_t cap = cols << shift;
   return n < 0 ? 0 : n > cap ? cap : n;
-}
-
-// Eight codes as bfloat16 numbers, exactly.
-template <int CT>
-__device__ __forceinline__ uint4 numbers(uint32_t lo, uint32_t hi) {
-  uint32_t w[4];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t c = h ? hi : lo;
-    if constexpr (CT == kCacheE4m3) {
-      w[2 * h] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false));
-      w[2 * h + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true));
-    } else {
-      // whole numbers of 8 bits: the upper half of their fp32 form holds them
-      float f[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] = (float)(int8_t)(c >> (8 * j));
-      w[2 * h] = __builtin_amdgcn_perm(__float_as_uint(f[1]), __float_as_uint(f[0]), 0x07060302u);
-      w[2 * h + 1] = __builtin_amdgcn_perm(__float_as_uint(f[3]), __float_as_uint(f[2]), 0x07060302u);
-    }
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // The pages of the two halves of a tile (-1: none, or behind the length).
@@ -382,9 +361,9 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs a) {
 template <int DP, int W, int CT>
 void attention_as(const KvAttnArgs& a, hipStream_t stream) {
   const int group = a.q_heads / a.c.kv_heads, qtiles = (group + 15) / 16;
-  const int64_t ptiles = a.psplits ? (a.S * group + 15) / 16 : 0;
-  const int own = qtiles * a.splits, wide = own > a.psplits ? own : a.psplits;
-  hipLaunchKernelGGL((kv_attention_kernel<DP, W, CT>), dim3((unsigned)(a.c.kv_heads * wide), (unsigned)(a.S + ptiles)),
+  const int64_t ptiles = a.psplits && !a.wide ? (a.S * group + 15) / 16 : 0;
+  const int own = qtiles * a.splits, per_head = ptiles && a.psplits > own ? a.psplits : own;
+  hipLaunchKernelGGL((kv_attention_kernel<DP, W, CT>), dim3((unsigned)(a.c.kv_heads * per_head), (unsigned)(a.S + ptiles)),
                      dim3(64 * W), 0, stream, a, qtiles, (int)ptiles);
 }
 
@@ -408,15 +387,20 @@ int waves_for(int64_t groups, int head_dim, int64_t max_len) {
 
 }  // namespace
 
+// A prefix of more rows than two narrow tiles goes to wide workgroups.
+static bool is_wide(int64_t rows) { return rows > 32; }
+
 KvParts kv_parts(const KvCache& c, int64_t S, int q_heads, int64_t table_cols, int64_t prefix_cols) {
   KvParts p;
   const int64_t max_len = table_cols << c.page_shift;
   p.own = paged_splits(S, q_heads, c.kv_heads, c.head_dim, max_len);
   p.prefix = 0;
   if (!prefix_cols || !S) return p;
-  const int64_t rows = S * (q_heads / c.kv_heads), groups = c.kv_heads * ((rows + 15) / 16);
-  int64_t n = (2 * 256 + groups - 1) / groups;
-  const int64_t least = 4 * kMinTiles * kTile, most = ((prefix_cols << c.page_shift) + least - 1) / least;
+  const int64_t rows = S * (q_heads / c.kv_heads), cap = prefix_cols << c.page_shift;
+  const bool wide = is_wide(rows);
+  const int64_t groups = c.kv_heads * (wide ? (rows + 127) / 128 : (rows + 15) / 16);
+  int64_t n = ((wide ? 1 : 2) * 256 + groups - 1) / groups;
+  const int64_t least = (wide ? 8 : 4) * kMinTiles * kTile, most = (cap + least - 1) / least;
   if (n > most) n = most;
   if (n > kMaxParts / 2) n = kMaxParts / 2;
   p.prefix = n < 1 ? 1 : (int)n;
@@ -428,7 +412,12 @@ hipError_t launch_kv_attention(const KvAttnArgs& args, hipStream_t stream) {
   KvAttnArgs a = args;
   const int64_t group = a.q_heads / a.c.kv_heads;
   a.waves = a.psplits ? 4 : waves_for(a.S * a.c.kv_heads * ((group + 15) / 16), a.c.head_dim, a.table_cols << a.c.page_shift);
-  a.pwaves = a.waves;
+  a.wide = a.psplits && is_wide(a.S * group);
+  a.pwaves = a.wide ? 8 : a.waves;
+  if (a.wide) {
+    const hipError_t e = launch_kv_prefix(a, stream);
+    if (e != hipSuccess) return e;
+  }
   if (a.c.type == kCacheInt8) attention_of<kCacheInt8>(a, stream);
   else if (a.c.type == kCacheE4m3) attention_of<kCacheE4m3>(a, stream);
   else attention_of<kCacheBf16>(a, stream);

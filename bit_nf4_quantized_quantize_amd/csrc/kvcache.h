@@ -52,6 +52,7 @@ struct KvAttnArgs {
   int64_t q_stride, S, table_cols, prefix_cols;
   int q_heads, splits, psplits;
   int waves, pwaves;  // per workgroup, set by the launcher
+  bool wide;          // the prefix in wide workgroups, set by the launcher
   float scale;
 };
 // The parts of a call without and with a shared prefix.
@@ -60,5 +61,7 @@ struct KvParts {
 };
 KvParts kv_parts(const KvCache& c, int64_t S, int q_heads, int64_t table_cols, int64_t prefix_cols);
 hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t stream);
+// The prefix's part for many rows, called by it.
+hipError_t launch_kv_prefix(const KvAttnArgs& a, hipStream_t stream);
 
 }  // namespace qlora

@@ -65,4 +65,19 @@ __device__ __forceinline__ void split(const float (&p)[8], bf16x8 (&part)[3]) {
   part[2] = upper(w);
 }
 
+// The same in two parts: the second is rounded, so 16 bits stay at least (2^-8 of
+// a remainder under 2^-7).
+__device__ __forceinline__ void split2(const float (&p)[8], bf16x8 (&part)[2]) {
+  uint32_t w[8];
+  float left[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    w[j] = __builtin_elementwise_sub_sat(__float_as_uint(p[j]), 1u) & 0xFFFF0000u;
+    left[j] = p[j] - __uint_as_float(w[j]);
+  }
+  part[0] = upper(w);
+  part[1] = __builtin_bit_cast(bf16x8, make_uint4(pack_bf2(left[0], left[1]), pack_bf2(left[2], left[3]),
+                                                  pack_bf2(left[4], left[5]), pack_bf2(left[6], left[7])));
+}
+
 }  // namespace qlora

@@ -58,6 +58,9 @@ int check_attention(const qlora_kv_cache* c, int64_t S, int32_t q_heads, int64_t
   for (int64_t cols : {prefix_cols, table_cols})
     if (cols < 0 || cols > kMaxRows || cols * c->page_size > kMaxRows)
       return fail(QLORA_ERR_INVALID_ARG, "%s: columns * page_size of a table must be in [0, 2^31)", fn);
+  // positions in the prefix are counted a step or two ahead in 32 bits
+  if (prefix_cols * c->page_size > kMaxRows - 4096)
+    return fail(QLORA_ERR_INVALID_ARG, "%s: prefix_cols * page_size must be at most 2^31 - 4097", fn);
   return QLORA_OK;
 }
 

@@ -22,14 +22,19 @@ __device__ __forceinline__ int64_t cut_length(int64_t n, int64_t cols, int shift
   return n < 0 ? 0 : n > cap ? cap : n;
 }
 
-// The pages of the two halves of a tile (-1: none, or behind the length).
+// The table's entries for the two halves of a tile.  Any tile may be asked for:
+// behind the table's end the last entry is read, and whether tokens are there is
+// asked when the pages are used.
 struct Halves {
   int32_t of[2];
 };
-__device__ __forceinline__ Halves halves_at(const int32_t* table, int64_t tok, int64_t n, int shift) {
+__device__ __forceinline__ Halves halves_at(const int32_t* table, int64_t cols, int64_t tok, int shift) {
   Halves p;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) p.of[h] = tok + 16 * h < n ? table[(tok + 16 * h) >> shift] : -1;
+  for (int h = 0; h < 2; ++h) {
+    const int64_t at = (tok + 16 * h) >> shift;
+    p.of[h] = table[at < cols ? at : cols - 1];
+  }
   return p;
 }
 
@@ -51,40 +56,54 @@ struct KvTile {
   bool ok[2];           // the halves lie in pages of the cache
 };
 
+// Where the halves' rows are; sets t.ok.
+struct Rows {
+  int64_t of[2];
+};
 template <int DP, int CT>
-__device__ __forceinline__ void load_tile(KvTile<DP, CT>& t, const KvCache& c, const Halves& p, int64_t tok, int kv,
-                                          int lane) {
+__device__ __forceinline__ Rows rows_at(KvTile<DP, CT>& t, const KvCache& c, const Halves& p, int64_t tok, int64_t n,
+                                        int kv) {
+  Rows r;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int32_t page = __builtin_amdgcn_readfirstlane(p.of[h]);
+    t.ok[h] = tok + 16 * h < n && page >= 0 && page < c.num_pages;
+    // without a page the loads go to the cache's first rows and count nothing
+    const int64_t first = (tok + 16 * h) & ((1 << c.page_shift) - 1);
+    r.of[h] = t.ok[h] ? (((int64_t)page * c.kv_heads + kv) << c.page_shift) + first : 0;
+  }
+  return r;
+}
+template <int DP, int CT>
+__device__ __forceinline__ void load_v(KvTile<DP, CT>& t, const KvCache& c, const Rows& row, int lane) {
   using Tile = KvTile<DP, CT>;
   typedef typename std::conditional<kCoded<CT>, uint8_t, uint16_t>::type Elem;
   constexpr int CH = DP / Tile::EV;
   const int d = c.head_dim;
-  int64_t row[2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int32_t page = __builtin_amdgcn_readfirstlane(p.of[h]);
-    t.ok[h] = page >= 0 && page < c.num_pages;
-    // without a page the loads go to the cache's first rows and count nothing
-    const int64_t first = (tok + 16 * h) & ((1 << c.page_shift) - 1);
-    row[h] = t.ok[h] ? (((int64_t)page * c.kv_heads + kv) << c.page_shift) + first : 0;
+  for (int i = 0; i < Tile::VI; ++i) {
+    const int idx = i * 64 + lane, r = idx / CH, e = idx % CH * Tile::EV;
+    t.v[i] = *reinterpret_cast<const uint4*>((const Elem*)c.v + ((r < 16 ? row.of[0] : row.of[1]) + (r & 15)) * d +
+                                             (e < d ? e : 0));
   }
+}
+template <int DP, int CT>
+__device__ __forceinline__ void load_k(KvTile<DP, CT>& t, const KvCache& c, const Rows& row, int lane) {
+  using Tile = KvTile<DP, CT>;
+  typedef typename std::conditional<kCoded<CT>, uint8_t, uint16_t>::type Elem;
+  const int d = c.head_dim;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const Elem* key = (const Elem*)c.k + (row[h] + (lane & 15)) * d;
+    const Elem* key = (const Elem*)c.k + (row.of[h] + (lane & 15)) * d;
 #pragma unroll
     for (int i = 0; i < Tile::KI; ++i) {
       const int e = (4 * i + (lane >> 4)) * Tile::EV;
       t.k[h][i] = *reinterpret_cast<const uint4*>(key + (e < d ? e : 0));
     }
     if constexpr (kCoded<CT>) {
-      t.ks[h] = *reinterpret_cast<const float4*>(c.k_scale + row[h] + 4 * (lane >> 4));
-      t.vs[h] = *reinterpret_cast<const float4*>(c.v_scale + row[h] + 4 * (lane >> 4));
+      t.ks[h] = *reinterpret_cast<const float4*>(c.k_scale + row.of[h] + 4 * (lane >> 4));
+      t.vs[h] = *reinterpret_cast<const float4*>(c.v_scale + row.of[h] + 4 * (lane >> 4));
     }
-  }
-#pragma unroll
-  for (int i = 0; i < Tile::VI; ++i) {
-    const int idx = i * 64 + lane, r = idx / CH, e = idx % CH * Tile::EV;
-    t.v[i] = *reinterpret_cast<const uint4*>((const Elem*)c.v + ((r < 16 ? row[0] : row[1]) + (r & 15)) * d +
-                                             (e < d ? e : 0));
   }
 }
 
@@ -102,14 +121,15 @@ __device__ __forceinline__ void place_of(const Columns& c, int col, int64_t* s, 
   if (c.s >= 0) {
     *s = c.s, *head = c.kv * c.group + (int)r;
   } else {
-    *s = r / c.group, *head = c.kv * c.group + (int)(r % c.group);
+    *s = (uint32_t)r / (uint32_t)c.group, *head = c.kv * c.group + (int)((uint32_t)r % (uint32_t)c.group);
   }
 }
 
-// Grid: y < ptiles are the prefix's tiles of 16 rows, then the sequences; x: kv
-// heads, tiles of heads and parts.
+// Grid: with ptiles tiles of 16 rows of a prefix first their kv heads and parts, then
+// the sequences' kv heads, tiles of heads and parts, all in x; else those in x and
+// the sequences in y.
 template <int DP, int W, int CT>
-__global__ __launch_bounds__(64 * W) void kv_attention_kernel(KvAttnArgs a, int qtiles, int ptiles) {
+__global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(KvAttnArgs a, int qtiles, int ptiles) {
   using Tile = KvTile<DP, CT>;
   constexpr int CH = DP / Tile::EV;
   constexpr int PITCH = DP + 16;  // of the V tile: 16 rows of one column go to different banks
@@ -123,37 +143,44 @@ __global__ __launch_bounds__(64 * W) void kv_attention_kernel(KvAttnArgs a, int 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, col = lane & 15, d = kc.head_dim;
   const int group = a.q_heads / kc.kv_heads, parts = a.psplits + a.splits;
-  const bool shared = (int)blockIdx.y < ptiles;
+  uint32_t id = blockIdx.x;
+  const uint32_t jobs = (uint32_t)kc.kv_heads * a.psplits, own = (uint32_t)(kc.kv_heads * qtiles) * a.splits;
+  const bool shared = id < ptiles * jobs;
   Columns cols;
   cols.group = group;
-  int id = blockIdx.x, z;
-  int64_t n;
+  int z;
+  int64_t n, table_cols;
   const int32_t* table;
-  Cut cut;
+  Cut32 cut;
+  Halves pages = {{-1, -1}};  // of the first tile, asked for beside the length where it does not depend on it
   if (shared) {
-    if (id >= kc.kv_heads * a.psplits) return;
-    z = id % a.psplits;
-    cols.kv = id / a.psplits;
-    cols.s = -1, cols.r0 = (int64_t)blockIdx.y * 16;
+    const uint32_t tile = id / jobs;
+    id -= tile * jobs;
+    z = id % (uint32_t)a.psplits;
+    cols.kv = id / (uint32_t)a.psplits;
+    cols.s = -1, cols.r0 = (int64_t)tile * 16;
     const int64_t left = a.S * group - cols.r0;
     cols.n = left < 16 ? (int)left : 16;
+    table = a.prefix_table, table_cols = a.prefix_cols;
+    if (z == 0) pages = halves_at(table, table_cols, wave * kTile, kc.page_shift);
     n = cut_length(*a.prefix_len, a.prefix_cols, kc.page_shift);
-    table = a.prefix_table;
-    cut = cut_of(n, a.psplits, W);
+    cut = cut32_of((uint32_t)n, a.psplits, W);
   } else {
-    if (id >= kc.kv_heads * qtiles * a.splits) return;
-    z = id % a.splits;
-    id /= a.splits;
-    const int qt = id % qtiles;
-    cols.kv = id / qtiles;
-    cols.s = blockIdx.y - ptiles, cols.r0 = qt * 16;
+    uint32_t s = blockIdx.y;
+    if (ptiles) id -= ptiles * jobs, s = id / own, id -= s * own;
+    z = id % (uint32_t)a.splits;
+    id /= (uint32_t)a.splits;
+    const int qt = id % (uint32_t)qtiles;
+    cols.kv = id / (uint32_t)qtiles;
+    cols.s = s, cols.r0 = qt * 16;
     cols.n = group - qt * 16 < 16 ? group - qt * 16 : 16;
+    table = a.table + cols.s * a.table_cols, table_cols = a.table_cols;
+    if (z == 0 && table_cols) pages = halves_at(table, table_cols, wave * kTile, kc.page_shift);
     n = cut_length(a.lengths[cols.s], a.table_cols, kc.page_shift);
-    table = a.table + cols.s * a.table_cols;
-    cut = cut_of(n, a.splits, W);
+    cut = cut32_of((uint32_t)n, a.splits, W);
   }
-  if (parts > 1 && z >= cut.parts) return;
-  const int64_t first = z * cut.per;
+  if (parts > 1 && (uint32_t)z >= cut.parts) return;
+  const int64_t first = (int64_t)z * cut.per;
   const int64_t last = first + cut.per < cut.tiles ? first + cut.per : cut.tiles;
 
   // Q^T: column col (a query row), reduction elements as the keys' lanes hold them
@@ -178,16 +205,21 @@ __global__ __launch_bounds__(64 * W) void kv_attention_kernel(KvAttnArgs a, int 
   for (int t = 0; t < DP / 16; ++t) acc[t] = (floatx4){0, 0, 0, 0};
   __bf16* vt = reinterpret_cast<__bf16*>(lds + wave * WAVE_BYTES);
 
-  // the loads of the next tile run under the products of this one, and the
-  // look-up of the pages after that, so neither waits for the other
+  // The loads of the next tile run under the products of this one, its values'
+  // from the moment that this one's are in LDS, and the look-up of the pages after
+  // that, so neither waits for the other.
   Tile t;
   int64_t ti = first + wave;
-  Halves pages = halves_at(table, ti * kTile, n, kc.page_shift);
-  if (ti < last) load_tile<DP, CT>(t, kc, pages, ti * kTile, cols.kv, lane);
-  pages = halves_at(table, (ti + W) * kTile, n, kc.page_shift);
+  if (ti < last) {
+    if (z) pages = halves_at(table, table_cols, ti * kTile, kc.page_shift);
+    const Rows r = rows_at(t, kc, pages, ti * kTile, n, cols.kv);
+    load_k(t, kc, r, lane);
+    load_v(t, kc, r, lane);
+    pages = halves_at(table, table_cols, (ti + W) * kTile, kc.page_shift);
+  }
   for (; ti < last; ti += W) {
     const int64_t tok = ti * kTile;
-    const bool full = tok + kTile <= n && t.ok[0] && t.ok[1];
+    const bool full = tok + kTile <= n && t.ok[0] && t.ok[1], more = ti + W < last;
     // V to LDS
     lds_in_order();
 #pragma unroll
@@ -202,6 +234,12 @@ __global__ __launch_bounds__(64 * W) void kv_attention_kernel(KvAttnArgs a, int 
       } else {
         dst[0] = v;
       }
+    }
+    const bool ok0 = t.ok[0], ok1 = t.ok[1];
+    Rows next;
+    if (more) {
+      next = rows_at(t, kc, pages, tok + W * kTile, n, cols.kv);
+      load_v(t, kc, next, lane);
     }
     // scores
     floatx4 sc[2];
@@ -220,15 +258,16 @@ __global__ __launch_bounds__(64 * W) void kv_attention_kernel(KvAttnArgs a, int 
         }
       }
     }
-    const bool ok0 = t.ok[0], ok1 = t.ok[1];
     float p[8], vs[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       p[j] = sc[j >> 2][j & 3] * (kCoded<CT> ? part_of(t.ks[j >> 2], j & 3) * scale2 : scale2);
       vs[j] = kCoded<CT> ? part_of(t.vs[j >> 2], j & 3) : 1.0f;
     }
-    if (ti + W < last) load_tile<DP, CT>(t, kc, pages, tok + W * kTile, cols.kv, lane);
-    pages = halves_at(table, tok + 2 * W * kTile, n, kc.page_shift);
+    if (more) {
+      load_k(t, kc, next, lane);
+      pages = halves_at(table, table_cols, tok + 2 * W * kTile, kc.page_shift);
+    }
     if (!full) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -305,66 +344,74 @@ __global__ __launch_bounds__(64 * W) void kv_attention_kernel(KvAttnArgs a, int 
   }
 }
 
-// Joins the parts of a row, one workgroup per sequence and head: its threads
-// hold four elements of the head each and take the parts in turns of 1024 /
-// head_dim, then the turns' sums are added in order.
+// Joins the parts of a row: TEAM waves each take the parts in turns, a turn being
+// as many parts as fit into the wave with four elements of the head per lane (256 /
+// head_dim); the turns' sums are added in order.  Four waves per workgroup.
 constexpr int kMaxParts = 256;
 
-__global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs a) {
-  __shared__ float s_f[kMaxParts], s_m[4], s_l[4];
-  __shared__ floatx4 s_o[256];
-  const int64_t s = blockIdx.y, row = s * a.q_heads + blockIdx.x;
-  const int d = a.c.head_dim, dq = d / 4, t = threadIdx.x, all = a.psplits + a.splits;
-  const int own = (int)cut_of(cut_length(a.lengths[s], a.table_cols, a.c.page_shift), a.splits, a.waves).parts;
+template <int TEAM>
+__global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs a, Div heads) {
+  __shared__ floatx4 s_o[TEAM > 1 ? TEAM : 1][64];
+  __shared__ float s_sum[TEAM > 1 ? TEAM : 1];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, member = wave % TEAM;
+  const int d = a.c.head_dim, dq = d / 4, all = a.psplits + a.splits;
+  const int64_t row = ((int64_t)blockIdx.x * 4 + wave) / TEAM;
+  if (row >= a.S * a.q_heads) return;  // never part of a team
+  const int s = (int)row / heads;
+  const int own = cut32_of((uint32_t)cut_length(a.lengths[s], a.table_cols, a.c.page_shift), a.splits, a.waves).parts;
   int pre = 0;
-  if (a.psplits) {
-    const int64_t n = cut_length(*a.prefix_len, a.prefix_cols, a.c.page_shift);
-    pre = (int)cut_of(n, a.psplits, a.pwaves).parts;
-  }
+  if (a.psplits)
+    pre = cut32_of((uint32_t)cut_length(*a.prefix_len, a.prefix_cols, a.c.page_shift), a.psplits, a.pwaves).parts;
   // part i of those there are lies at i, behind the prefix's at psplits ..
   const int parts = pre + own, gap = a.psplits - pre;
-  float m = -INFINITY, l = 0.0f;
-  if (t < parts) {
-    const float2 v = *reinterpret_cast<const float2*>(a.part_ml + (row * all + (t < pre ? t : t + gap)) * 2);
-    m = v.x, l = v.y;
-  }
-  const float wm = wave_max(m);
-  if ((t & 63) == 0) s_m[t >> 6] = wm;
-  __syncthreads();
-  const float mx = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3])), mu = mx == -INFINITY ? 0.0f : mx;
-  const float f = __builtin_amdgcn_exp2f(m - mu);
-  l *= f;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) l += __shfl_xor(l, o, 64);
-  s_f[t] = f;
-  if ((t & 63) == 0) s_l[t >> 6] = l;
-  __syncthreads();
-  const float sum = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]), inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  if (a.lse && t == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994530942f;
-  const int turns = 256 / dq, turn = t / dq, c = t - turn * dq;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row * all;
+  float m = -INFINITY;
+  for (int i = lane; i < parts; i += 64) m = fmaxf(m, ml[i < pre ? i : i + gap].x);
+  const float mx = wave_max(m), mu = mx == -INFINITY ? 0.0f : mx;
+  const int turns = 64 / dq, turn = lane / dq, c = lane - turn * dq;
+  float sum = 0.0f;
   floatx4 o = {0, 0, 0, 0};
   if (turn < turns) {
     const float* src = a.part_o + row * all * d + 4 * c;
-#pragma unroll 4
-    for (int z = turn; z < parts; z += turns)
-      o += *reinterpret_cast<const floatx4*>(src + (int64_t)(z < pre ? z : z + gap) * d) * s_f[z];
+#pragma unroll 8
+    for (int i = member * turns + turn; i < parts; i += TEAM * turns) {
+      const int at = i < pre ? i : i + gap;
+      const float2 v = ml[at];
+      const float f = __builtin_amdgcn_exp2f(v.x - mu);
+      sum += v.y * f;
+      o += *reinterpret_cast<const floatx4*>(src + (int64_t)at * d) * f;
+    }
   }
-  s_o[t] = o;
-  __syncthreads();
-  if (t < dq) {
-    for (int k = 1; k < turns; ++k) o += s_o[k * dq + t];
-    o *= inv;
-    *reinterpret_cast<uint2*>(a.out + row * d + 4 * t) = make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
+  // the other turns' lanes hold the same elements
+  float all_sum = sum;
+  floatx4 all_o = o;
+  for (int k = 1; k < turns; ++k) {
+    const int from = k * dq + c;
+    all_sum += __shfl(sum, from, 64);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) all_o[j] += __shfl(o[j], from, 64);
   }
+  if constexpr (TEAM > 1) {
+    s_o[member][lane] = all_o;
+    if (lane == 0) s_sum[member] = all_sum;
+    __syncthreads();
+    if (member > 0) return;
+#pragma unroll
+    for (int k = 1; k < TEAM; ++k) all_o += s_o[k][lane], all_sum += s_sum[k];
+  }
+  if (lane >= dq) return;
+  all_o *= all_sum == 0.0f ? 0.0f : 1.0f / all_sum;
+  *reinterpret_cast<uint2*>(a.out + row * d + 4 * lane) = make_uint2(pack_bf2(all_o[0], all_o[1]), pack_bf2(all_o[2], all_o[3]));
+  if (a.lse && lane == 0) a.lse[row] = all_sum == 0.0f ? -INFINITY : (mx + log2f(all_sum)) * 0.69314718055994530942f;
 }
 
 template <int DP, int W, int CT>
 void attention_as(const KvAttnArgs& a, hipStream_t stream) {
   const int group = a.q_heads / a.c.kv_heads, qtiles = (group + 15) / 16;
   const int64_t ptiles = a.psplits && !a.wide ? (a.S * group + 15) / 16 : 0;
-  const int own = qtiles * a.splits, per_head = ptiles && a.psplits > own ? a.psplits : own;
-  hipLaunchKernelGGL((kv_attention_kernel<DP, W, CT>), dim3((unsigned)(a.c.kv_heads * per_head), (unsigned)(a.S + ptiles)),
-                     dim3(64 * W), 0, stream, a, qtiles, (int)ptiles);
+  const int64_t own = (int64_t)a.c.kv_heads * qtiles * a.splits, jobs = ptiles * a.c.kv_heads * a.psplits;
+  const dim3 grid = ptiles ? dim3((unsigned)(jobs + a.S * own)) : dim3((unsigned)own, (unsigned)a.S);
+  hipLaunchKernelGGL((kv_attention_kernel<DP, W, CT>), grid, dim3(64 * W), 0, stream, a, qtiles, (int)ptiles);
 }
 
 template <int DP, int CT>
@@ -387,8 +434,9 @@ int waves_for(int64_t groups, int head_dim, int64_t max_len) {
 
 }  // namespace
 
-// A prefix of more rows than two narrow tiles goes to wide workgroups.
-static bool is_wide(int64_t rows) { return rows > 32; }
+// Rows of a prefix's workgroup: narrow ones (0) up to 32.
+static int wide_rows(int64_t rows, int head_dim) { return rows <= 32 ? 0 : rows <= 128 || head_dim > 128 ? 128 : 256; }
+constexpr int kWideWaves = 2;  // a part of the prefix has the tiles of that many narrow waves at least
 
 KvParts kv_parts(const KvCache& c, int64_t S, int q_heads, int64_t table_cols, int64_t prefix_cols) {
   KvParts p;
@@ -397,10 +445,10 @@ KvParts kv_parts(const KvCache& c, int64_t S, int q_heads, int64_t table_cols, i
   p.prefix = 0;
   if (!prefix_cols || !S) return p;
   const int64_t rows = S * (q_heads / c.kv_heads), cap = prefix_cols << c.page_shift;
-  const bool wide = is_wide(rows);
-  const int64_t groups = c.kv_heads * (wide ? (rows + 127) / 128 : (rows + 15) / 16);
+  const int wide = wide_rows(rows, c.head_dim);
+  const int64_t groups = c.kv_heads * (wide ? (rows + wide - 1) / wide : (rows + 15) / 16);
   int64_t n = ((wide ? 1 : 2) * 256 + groups - 1) / groups;
-  const int64_t least = (wide ? 8 : 4) * kMinTiles * kTile, most = (cap + least - 1) / least;
+  const int64_t least = (wide ? kWideWaves : 4) * kMinTiles * kTile, most = (cap + least - 1) / least;
   if (n > most) n = most;
   if (n > kMaxParts / 2) n = kMaxParts / 2;
   p.prefix = n < 1 ? 1 : (int)n;
@@ -412,8 +460,8 @@ hipError_t launch_kv_attention(const KvAttnArgs& args, hipStream_t stream) {
   KvAttnArgs a = args;
   const int64_t group = a.q_heads / a.c.kv_heads;
   a.waves = a.psplits ? 4 : waves_for(a.S * a.c.kv_heads * ((group + 15) / 16), a.c.head_dim, a.table_cols << a.c.page_shift);
-  a.wide = a.psplits && is_wide(a.S * group);
-  a.pwaves = a.wide ? 8 : a.waves;
+  a.wide = a.psplits ? wide_rows(a.S * group, a.c.head_dim) : 0;
+  a.pwaves = a.wide ? kWideWaves : a.waves;
   if (a.wide) {
     const hipError_t e = launch_kv_prefix(a, stream);
     if (e != hipSuccess) return e;
@@ -422,7 +470,15 @@ hipError_t launch_kv_attention(const KvAttnArgs& args, hipStream_t stream) {
   else if (a.c.type == kCacheE4m3) attention_of<kCacheE4m3>(a, stream);
   else attention_of<kCacheBf16>(a, stream);
   if (a.psplits + a.splits > 1)
-    hipLaunchKernelGGL(kv_join_kernel, dim3(a.q_heads, (unsigned)a.S), dim3(256), 0, stream, a);
+  {
+    // a wave per row once the rows fill the card (4096 rows of 9 parts: 7.0 us, with
+    // four waves 12.6; 512 rows of 16: 9.5 and 4.2)
+    const int64_t rows = a.S * a.q_heads;
+    if (rows >= 2048)
+      hipLaunchKernelGGL(kv_join_kernel<1>, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a, div_by(a.q_heads));
+    else
+      hipLaunchKernelGGL(kv_join_kernel<4>, dim3((unsigned)rows), dim3(256), 0, stream, a, div_by(a.q_heads));
+  }
   return hipGetLastError();
 }
 

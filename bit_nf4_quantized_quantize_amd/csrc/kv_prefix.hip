@@ -12,71 +12,140 @@ namespace qlora {
 
 namespace {
 
-// A workgroup takes 32 WQ rows and a part of the prefix: WQ waves with 32 rows
-// each, WT of them for each row, which share the tokens of a step.
+// A workgroup takes 32 WQ rows, 32 to a wave, and a part of the prefix in steps
+// of TT = 32 WT NS tokens, of which WT waves of the same rows take 32 NS each:
 //   scores^T [32 tokens x 32 rows] = K Q^T,  out^T [d x 32 rows] += V^T P
 // with K and V of a step as bfloat16 in LDS.
-template <int DP, int CT, int WQ, int WT, int SUB>
+//
+// A matrix instruction keeps its unit busy for 32 cycles and the issue for 4, and
+// the softmax of a tile has about six vector instructions for each of its matrix
+// ones, so a wave has to issue both kinds in turn.  Tile i (32 tokens) is taken
+// in three blocks: its scores are formed in block i - 1, its weights in block i,
+// its part of the output in block i + 1; within a block nothing depends on
+// anything but the last ones' results.
+template <int DP, int CT, int WQ, int WT, int NS>
 struct Wide {
   static constexpr int THREADS = 64 * WQ * WT;
-  static constexpr int TT = 32 * WT * SUB;             // tokens of a step
+  static constexpr int TT = 32 * WT * NS;              // tokens of a step
   static constexpr int KP = DP + 8, VP = DP + 16;      // pitches
   static constexpr int EV = CT == kCacheBf16 ? 8 : 16; // elements in 16 bytes
   static constexpr int CH = DP / EV;                   // 16-byte pieces of a padded row
   static constexpr int PER = (TT * CH + THREADS - 1) / THREADS;
-  static constexpr int OP = DP + 4;
-  struct Step {
-    __bf16 k[TT * KP];
-    __bf16 v[TT * VP];
-    float ks[TT], vs[TT], bias[TT];
-    int ok[TT / 16];
+  // Between two barriers the waves are within NS blocks of each other: they read
+  // keys of one step, values of up to two or of the one three before that which
+  // is written.
+  static constexpr int NK = 2, NV = NS == 1 ? 4 : 3;
+  struct Lds {
+    __bf16 k[NK][TT * KP];
+    __bf16 v[NV][TT * VP];
+    float ks[NK][TT], vs[NV][TT], bias[NK][TT];
+    int ok[NK][TT / 16];
   };
-  static constexpr int BYTES0 = 2 * sizeof(Step);
-  static constexpr int JOIN = WT > 1 ? (WT - 1) * WQ * 32 * (OP + 2) * 4 : 0;
-  static constexpr int BYTES = BYTES0 > JOIN ? BYTES0 : JOIN;
+  static constexpr int OP = DP + 6;  // of what a wave leaves for another: outputs, maximum and sum
+  static constexpr int JOIN = (WT - 1) * WQ * 32 * OP * 4;
+  static constexpr int BYTES = (int)sizeof(Lds) > JOIN ? (int)sizeof(Lds) : JOIN;
 };
 
-// What a thread brings in of a step.
+// What a thread brings in of a step, and the pages (-1: none) it will do so from
+// in the next one.
 template <class W>
 struct Load {
   uint4 k[W::PER], v[W::PER];
   bool ok[W::PER];
   float ks, vs;
   bool in;
+  int32_t page[W::PER], row_page;
 };
 
-template <int DP, int CT, int WQ, int WT, int SUB>
-__global__ __launch_bounds__(64 * WQ * WT) void kv_prefix_kernel(KvAttnArgs a, int row_tiles) {
-  using W = Wide<DP, CT, WQ, WT, SUB>;
+__device__ __forceinline__ int64_t prefix_of(const KvAttnArgs& a) {
+  const int64_t n = *a.prefix_len, cap = a.prefix_cols << a.c.page_shift;
+  return n < 0 ? 0 : n > cap ? cap : n;
+}
+
+template <int DP, int CT, int WQ, int WT, int NS>
+__global__ __launch_bounds__(64 * WQ * WT) void kv_prefix_kernel(KvAttnArgs a) {
+  using W = Wide<DP, CT, WQ, WT, NS>;
   typedef typename std::conditional<CT == kCacheBf16, uint16_t, uint8_t>::type Elem;
   constexpr bool CODED = CT != kCacheBf16;
-  __shared__ __attribute__((aligned(16))) char lds[W::BYTES];
-  typename W::Step* steps = reinterpret_cast<typename W::Step*>(lds);
+  __shared__ __attribute__((aligned(16))) char bytes[W::BYTES];
+  typename W::Lds& lds = *reinterpret_cast<typename W::Lds*>(bytes);
 
   const KvCache& c = a.c;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wq = wave % WQ, wt = wave / WQ, hi = lane >> 5, d = c.head_dim;
+  const int mine = 32 * NS * wt;  // of the tokens of a step
   const int group = a.q_heads / c.kv_heads, parts = a.psplits + a.splits;
-  int id = blockIdx.x;
-  const int z = id % a.psplits;
-  id /= a.psplits;
-  const int kv = id % c.kv_heads, rt = id / c.kv_heads;
-  const int64_t rows = a.S * group, row = (int64_t)rt * 32 * WQ + 32 * wq + (lane & 31);
-  const bool busy = (int64_t)rt * 32 * WQ + 32 * wq < rows;  // the wave has rows
-  const int64_t cap = a.prefix_cols << c.page_shift;
-  int64_t n = *a.prefix_len;
-  n = n < 0 ? 0 : n > cap ? cap : n;
-  const Cut cut = cut_of(n, a.psplits, a.pwaves);
-  if (z >= cut.parts) return;
-  const int64_t first = z * cut.per * kTile;
-  int64_t last = first + cut.per * kTile;
-  if (last > n) last = n;
+  uint32_t id = blockIdx.x;
+  const int z = id % (uint32_t)a.psplits;
+  id /= (uint32_t)a.psplits;
+  const int kv = id % (uint32_t)c.kv_heads, rt = id / (uint32_t)c.kv_heads;
+  const int rows = (int)a.S * group, row = (rt * WQ + wq) * 32 + (lane & 31);  // under 65536 * 4096
+  const int n = (int)prefix_of(a);
+  const Cut32 cut = cut32_of(n, a.psplits, a.pwaves);
+  if ((uint32_t)z >= cut.parts) return;
+  const int first = z * (int)cut.per * kTile, last = n - first < (int)cut.per * kTile ? n : first + (int)cut.per * kTile;
 
+  Load<W> ld;
+  const int in_page = (1 << c.page_shift) - 1;
+  const uint32_t page_rows = (uint32_t)c.kv_heads << c.page_shift;
+  const int64_t kv_row = (int64_t)kv << c.page_shift;
+  // The page of a token, as the table has it; whether it is one is asked when it
+  // is used, a step later, so that nothing waits for it here.
+  auto entry = [&](int tok) { return a.prefix_table[(tok < last ? tok : last - 1) >> c.page_shift]; };
+  auto there = [&](int32_t page, int tok) { return tok < last && page >= 0 && page < c.num_pages; };
+  auto look_up = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < W::PER; ++i) ld.page[i] = entry(t0 + (i * W::THREADS + tid) / W::CH);
+    if (tid < W::TT) ld.row_page = entry(t0 + tid);
+  };
+  // Rows that are not there are read from the cache's first ones and put as zeros.
+  auto load = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < W::PER; ++i) {
+      const int idx = i * W::THREADS + tid, r = idx / W::CH, e = idx % W::CH * W::EV;
+      ld.ok[i] = e < d && there(ld.page[i], t0 + r);
+      const int64_t at = ((int64_t)ld.page[i] * page_rows + kv_row + ((t0 + r) & in_page)) * d + e;
+      ld.k[i] = *reinterpret_cast<const uint4*>((const Elem*)c.k + (ld.ok[i] ? at : 0));
+      ld.v[i] = *reinterpret_cast<const uint4*>((const Elem*)c.v + (ld.ok[i] ? at : 0));
+    }
+    ld.in = tid < W::TT && there(ld.row_page, t0 + tid);
+    if (CODED && tid < W::TT) {
+      const int64_t at = ld.in ? (int64_t)ld.row_page * page_rows + kv_row + ((t0 + tid) & in_page) : 0;
+      ld.ks = c.k_scale[at], ld.vs = c.v_scale[at];
+    }
+  };
+  const float scale2 = a.scale * 1.44269504088896340736f;  // scores in base 2
+  auto store = [&](int nk, int nv) {
+#pragma unroll
+    for (int i = 0; i < W::PER; ++i) {
+      const int idx = i * W::THREADS + tid, r = idx / W::CH, e = idx % W::CH * W::EV;
+      if (W::TT * W::CH % W::THREADS && r >= W::TT) continue;
+      uint4* k = reinterpret_cast<uint4*>(lds.k[nk] + r * W::KP + e);
+      uint4* v = reinterpret_cast<uint4*>(lds.v[nv] + r * W::VP + e);
+      uint4 kk = ld.k[i], vv = ld.v[i];
+      if (!ld.ok[i]) kk = vv = make_uint4(0, 0, 0, 0);
+      if constexpr (CODED) {
+        k[0] = numbers<CT>(kk.x, kk.y), k[1] = numbers<CT>(kk.z, kk.w);
+        v[0] = numbers<CT>(vv.x, vv.y), v[1] = numbers<CT>(vv.z, vv.w);
+      } else {
+        k[0] = kk, v[0] = vv;
+      }
+    }
+    if (tid < W::TT) {
+      lds.ks[nk][tid] = CODED ? (ld.in ? ld.ks * scale2 : 0.0f) : scale2;
+      lds.vs[nv][tid] = ld.in ? ld.vs : 0.0f;
+      lds.bias[nk][tid] = ld.in ? 0.0f : -INFINITY;
+      // the last token of sixteen is there: so are the others of its page
+      if ((tid & 15) == 15) lds.ok[nk][tid >> 4] = ld.in;
+    }
+  };
+
+  look_up(first);
   // Q^T: column lane % 32 (a row), reduction elements 16 i + 8 (lane / 32) ..
   bf16x8 q[DP / 16];
   int64_t seq = 0;
   int head = 0;
-  if (row < rows) seq = row / group, head = kv * group + (int)(row % group);
+  if (row < rows) seq = (uint32_t)row / (uint32_t)group, head = kv * group + (int)((uint32_t)row % (uint32_t)group);
 #pragma unroll
   for (int i = 0; i < DP / 16; ++i) {
     const int e = 16 * i + 8 * hi;
@@ -84,183 +153,179 @@ __global__ __launch_bounds__(64 * WQ * WT) void kv_prefix_kernel(KvAttnArgs a, i
     if (row < rows && e < d) v = *reinterpret_cast<const uint4*>(a.q + seq * a.q_stride + (int64_t)head * d + e);
     q[i] = __builtin_bit_cast(bf16x8, v);
   }
-  const float scale2 = a.scale * 1.44269504088896340736f;  // scores in base 2
+  // the values of the step before the first are zeros, with weights of zero
+  for (int i = tid; i < W::TT * W::VP / 8; i += W::THREADS)
+    reinterpret_cast<uint4*>(lds.v[W::NV - 1])[i] = make_uint4(0, 0, 0, 0);
+  load(first);
+  look_up(first + W::TT);
+  store(0, 0);
+  load(first + W::TT);
+  look_up(first + 2 * W::TT);
+  __syncthreads();
+
+  // m: of the weights so far, a whole number, so that scaling by another is exact
   float m = -INFINITY, l = 0.0f;
   floatx16 acc[DP / 32];
 #pragma unroll
   for (int t = 0; t < DP / 32; ++t)
 #pragma unroll
     for (int j = 0; j < 16; ++j) acc[t][j] = 0.0f;
+  float x[16];            // scores of the tile less m, in base 2
+  bf16x8 part[2][2] = {};  // weights of the tile before it: steps of 16 tokens, parts
 
-  Load<W> ld;
-  auto load = [&](int64_t t0) {
+  // A tile's scores less m, and the largest
+  auto scores = [&](const floatx16& sc, const float* ks, float* top) {
+    const float mu = m == -INFINITY ? 0.0f : m;
+    float t = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < W::PER; ++i) {
-      const int idx = i * W::THREADS + tid, r = idx / W::CH, e = idx % W::CH * W::EV;
-      const int64_t tok = t0 + r;
-      ld.ok[i] = false;
-      ld.k[i] = ld.v[i] = make_uint4(0, 0, 0, 0);
-      if (r >= W::TT || tok >= last) continue;
-      const int32_t page = a.prefix_table[tok >> c.page_shift];
-      ld.ok[i] = page >= 0 && page < c.num_pages;
-      if (!ld.ok[i] || e >= d) continue;
-      const int64_t at = ((((int64_t)page * c.kv_heads + kv) << c.page_shift) + (tok & ((1 << c.page_shift) - 1))) * d + e;
-      ld.k[i] = *reinterpret_cast<const uint4*>((const Elem*)c.k + at);
-      ld.v[i] = *reinterpret_cast<const uint4*>((const Elem*)c.v + at);
+    for (int b = 0; b < 4; ++b) {
+      const floatx4 f = *reinterpret_cast<const floatx4*>(ks + 8 * b + 4 * hi);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[4 * b + j] = fmaf(sc[4 * b + j], f[j], -mu);
     }
-    if (tid < W::TT) {
-      const int64_t tok = t0 + tid;
-      ld.ks = 0.0f, ld.vs = 0.0f, ld.in = false;
-      if (tok < last) {
-        const int32_t page = a.prefix_table[tok >> c.page_shift];
-        ld.in = page >= 0 && page < c.num_pages;
-        if (CODED && ld.in) {
-          const int64_t at = (((int64_t)page * c.kv_heads + kv) << c.page_shift) + (tok & ((1 << c.page_shift) - 1));
-          ld.ks = c.k_scale[at], ld.vs = c.v_scale[at];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) t = fmaxf(t, x[j]);
+    *top = t;
+  };
+  // What is seldom: tokens that are not there, and a larger maximum.  m stays
+  // while no weight passes 2^8, which takes nothing from their precision.
+  auto settle = [&](int ok, const float* bias, float top) {
+    if (!__builtin_amdgcn_readfirstlane(ok)) {
+      top = -INFINITY;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const floatx4 f = *reinterpret_cast<const floatx4*>(bias + 8 * b + 4 * hi);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (f[j] != 0.0f) x[4 * b + j] = f[j];
+          top = fmaxf(top, x[4 * b + j]);
         }
       }
     }
-  };
-  auto store = [&](typename W::Step& s) {
+    if (!__ballot(top > 8.0f || m == -INFINITY)) return;
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    const bool up = top > 8.0f || (m == -INFINITY && top > -INFINITY);
+    if (!__ballot(up)) return;
+    const float by = up ? ceilf(top) : 0.0f;  // m moves by it
+    const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(-by);
+    if (up) m = (m == -INFINITY ? 0.0f : m) + by;
+    l *= f;
 #pragma unroll
-    for (int i = 0; i < W::PER; ++i) {
-      const int idx = i * W::THREADS + tid, r = idx / W::CH, e = idx % W::CH * W::EV;
-      if (r >= W::TT) continue;
-      uint4* k = reinterpret_cast<uint4*>(s.k + r * W::KP + e);
-      uint4* v = reinterpret_cast<uint4*>(s.v + r * W::VP + e);
-      if constexpr (CODED) {
-        k[0] = numbers<CT>(ld.k[i].x, ld.k[i].y), k[1] = numbers<CT>(ld.k[i].z, ld.k[i].w);
-        v[0] = numbers<CT>(ld.v[i].x, ld.v[i].y), v[1] = numbers<CT>(ld.v[i].z, ld.v[i].w);
-      } else {
-        k[0] = ld.k[i], v[0] = ld.v[i];
-      }
-    }
-    if (tid < W::TT) {
-      s.ks[tid] = ld.ks * scale2, s.vs[tid] = ld.vs, s.bias[tid] = ld.in ? 0.0f : -INFINITY;
-      // the last token of sixteen is there: so are the others of its page
-      if ((tid & 15) == 15) s.ok[tid >> 4] = ld.in;
-    }
+    for (int t = 0; t < DP / 32; ++t)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) acc[t][j] *= f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] -= by;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) part[h][k][j] = (__bf16)((float)part[h][k][j] * f);
   };
+  // V^T of 16 tokens: reduction slot e of a lane is token 8 (e / 4) + 4 hi + e %
+  // 4, as the scores have them
+  auto read_v = [&](const __bf16* v, int h, int t) {
+    const int g = lane >> 4, y = lane & 15;
+    const __bf16* src = v + (16 * h + 4 * hi + (y >> 2)) * W::VP + 16 * (g & 1) + 4 * (y & 3) + 32 * t;
+    const short8_t f = __builtin_shufflevector(ds_read_tr16(src), ds_read_tr16(src + 8 * W::VP), 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_bit_cast(bf16x8, f);
+  };
+  auto weighted = [&](const __bf16* v) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int t = 0; t < DP / 32; ++t) {
+        const bf16x8 f = read_v(v, h, t);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) acc[t] = mfma32(f, part[h][k], acc[t]);
+      }
+  };
+  auto products = [&](const __bf16* k) {
+    floatx16 sc;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) sc[j] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i) sc = mfma32(frag_kc(k, W::KP, 0, 16 * i, lane), q[i], sc);
+    return sc;
+  };
+  auto whole = [&](int nk, int tok) { return lds.ok[nk][tok / 16] & lds.ok[nk][tok / 16 + 1]; };
 
-  load(first);
-  store(steps[0]);
-  __syncthreads();
-  int buf = 0;
-  for (int64_t t0 = first; t0 < last; t0 += W::TT, buf ^= 1) {
-    const bool more = t0 + W::TT < last;
-    if (more) load(t0 + W::TT);
-    const typename W::Step& s = steps[buf];
-    if (busy) {
-      bool full = true;
-#pragma unroll
-      for (int i = 0; i < W::TT / 16; ++i) full &= s.ok[i] != 0;
-      full = __builtin_amdgcn_readfirstlane(full);
-      float p[SUB][16];
-      const int base = 32 * SUB * wt;
-#pragma unroll
-      for (int u = 0; u < SUB; ++u) {
-        floatx16 sc;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) sc[j] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < DP / 16; ++i) sc = mfma32(frag_kc(s.k, W::KP, base + 32 * u, 16 * i, lane), q[i], sc);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) p[u][j] = sc[j];
-        if constexpr (CODED) {
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const floatx4 ks = *reinterpret_cast<const floatx4*>(s.ks + base + 32 * u + 8 * b + 4 * hi);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) p[u][4 * b + j] *= ks[j];
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) p[u][j] *= scale2;
-        }
-        if (!full) {
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const floatx4 bias = *reinterpret_cast<const floatx4*>(s.bias + base + 32 * u + 8 * b + 4 * hi);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) p[u][4 * b + j] = bias[j] != 0.0f ? bias[j] : p[u][4 * b + j];
-          }
-        }
-      }
-      float mt = m;
-#pragma unroll
-      for (int u = 0; u < SUB; ++u)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) mt = fmaxf(mt, p[u][j]);
-      mt = fmaxf(mt, __shfl_xor(mt, 32, 64));
-      if (__ballot(mt > m)) {
-        const float old = __builtin_amdgcn_exp2f(m - (mt == -INFINITY ? 0.0f : mt));
-        l *= old;
-#pragma unroll
-        for (int t = 0; t < DP / 32; ++t)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) acc[t][j] *= old;
-        m = mt;
-      }
-      const float mu = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-      for (int u = 0; u < SUB; ++u) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          p[u][j] = __builtin_amdgcn_exp2f(p[u][j] - mu);
-          l += p[u][j];
-        }
-        if constexpr (CODED) {
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const floatx4 vs = *reinterpret_cast<const floatx4*>(s.vs + base + 32 * u + 8 * b + 4 * hi);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) p[u][4 * b + j] *= vs[j];
-          }
-        }
-#pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2) {
-          float w[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) w[j] = p[u][8 * k2 + j];
-          bf16x8 part[2];
-          split2(w, part);
-          const int g = lane >> 4, x = lane & 15;
-          // reduction slot e of a lane is token 8 (e / 4) + 4 hi + e % 4, as the scores have them
-          const __bf16* src = s.v + (base + 32 * u + 16 * k2 + 4 * hi + (x >> 2)) * W::VP + 16 * (g & 1) + 4 * (x & 3);
-#pragma unroll
-          for (int t = 0; t < DP / 32; ++t) {
-            const short4_t v0 = ds_read_tr16(src + 32 * t), v1 = ds_read_tr16(src + 32 * t + 8 * W::VP);
-            const short8_t v = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) acc[t] = mfma32(__builtin_bit_cast(bf16x8, v), part[k], acc[t]);
-          }
-        }
-      }
-    }
-    if (more) store(steps[buf ^ 1]);
-    __syncthreads();
+  {
+    float top;
+    scores(products(lds.k[0] + mine * W::KP), lds.ks[0] + mine, &top);
+    settle(whole(0, mine), lds.bias[0] + mine, top);
   }
+  // nv: buffers of the values of the step before this one, this one and the next
+  int nk = 0, nv[3] = {W::NV - 1, 0, 1};
+  for (int t0 = first; t0 < last; t0 += W::TT) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      if (s == NS - 1) {
+        // the keys of the next step are needed from here on
+        store(nk ^ 1, nv[2]);
+        load(t0 + 2 * W::TT);
+        look_up(t0 + 3 * W::TT);
+        __syncthreads();
+      }
+      const int kb = s == NS - 1 ? nk ^ 1 : nk, next = mine + (s == NS - 1 ? 0 : 32 * (s + 1));
+      const floatx16 sc = products(lds.k[kb] + next * W::KP);
+      weighted(lds.v[s == 0 ? nv[0] : nv[1]] + (mine + (s == 0 ? 32 * (NS - 1) : 32 * (s - 1))) * W::VP);
+      // weights of this tile
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        x[j] = __builtin_amdgcn_exp2f(x[j]);
+        l += x[j];
+      }
+      if constexpr (CODED) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const floatx4 f = *reinterpret_cast<const floatx4*>(lds.vs[nv[1]] + mine + 32 * s + 8 * b + 4 * hi);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[4 * b + j] *= f[j];
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = x[8 * h + j];
+        split2<!CODED>(w, part[h]);
+      }
+      float top;
+      scores(sc, lds.ks[kb] + next, &top);
+      // the weights are formed here, beside the products, not where they are used
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) asm volatile("" : "+v"(part[h][k]));
+      settle(whole(kb, next), lds.bias[kb] + next, top);
+    }
+    nk ^= 1;
+    nv[0] = nv[1], nv[1] = nv[2], nv[2] = nv[2] + 1 == W::NV ? 0 : nv[2] + 1;
+  }
+  weighted(lds.v[nv[0]] + (mine + 32 * (NS - 1)) * W::VP);
 
   l += __shfl_xor(l, 32, 64);
   if constexpr (WT > 1) {  // the waves of the same rows join, in order
-    float* all = reinterpret_cast<float*>(lds);
-    constexpr int ROW = W::OP + 2;
+    __syncthreads();
+    float* const all = reinterpret_cast<float*>(bytes) + (wq * 32 + (lane & 31)) * W::OP;
     if (wt > 0) {
-      float* o = all + (((wt - 1) * WQ + wq) * 32 + (lane & 31)) * ROW;
+      float* o = all + (wt - 1) * WQ * 32 * W::OP;
 #pragma unroll
       for (int t = 0; t < DP / 32; ++t)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[32 * t + acc_row32(j, lane)] = acc[t][j];
-      if (hi == 0) o[W::OP] = m, o[W::OP + 1] = l;
+      if (hi == 0) o[DP] = m, o[DP + 1] = l;
     }
     __syncthreads();
     if (wt > 0) return;
 #pragma unroll
     for (int w = 1; w < WT; ++w) {
-      const float* o = all + (((w - 1) * WQ + wq) * 32 + (lane & 31)) * ROW;
-      const float om = o[W::OP], mx = fmaxf(m, om), mu = mx == -INFINITY ? 0.0f : mx;
+      const float* o = all + (w - 1) * WQ * 32 * W::OP;
+      const float om = o[DP], mx = fmaxf(m, om), mu = mx == -INFINITY ? 0.0f : mx;
       const float f0 = __builtin_amdgcn_exp2f(m - mu), f1 = __builtin_amdgcn_exp2f(om - mu);
-      m = mx, l = l * f0 + o[W::OP + 1] * f1;
+      m = mx, l = l * f0 + o[DP + 1] * f1;
 #pragma unroll
       for (int t = 0; t < DP / 32; ++t)
 #pragma unroll
@@ -281,31 +346,37 @@ __global__ __launch_bounds__(64 * WQ * WT) void kv_prefix_kernel(KvAttnArgs a, i
   if (hi == 0) a.part_ml[at * 2] = m, a.part_ml[at * 2 + 1] = l;
 }
 
-template <int DP, int CT, int WQ, int WT, int SUB>
+template <int DP, int CT, int WQ, int WT, int NS>
 hipError_t prefix_as(const KvAttnArgs& a, hipStream_t stream) {
-  using W = Wide<DP, CT, WQ, WT, SUB>;
+  using W = Wide<DP, CT, WQ, WT, NS>;
   static_assert(W::BYTES <= 160 * 1024, "LDS of a CU");
-  const auto kernel = kv_prefix_kernel<DP, CT, WQ, WT, SUB>;
   const int64_t rows = a.S * (a.q_heads / a.c.kv_heads), tiles = (rows + 32 * WQ - 1) / (32 * WQ);
-  hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles * a.c.kv_heads * a.psplits)), dim3(W::THREADS), 0, stream, a,
-                     (int)tiles);
+  hipLaunchKernelGGL((kv_prefix_kernel<DP, CT, WQ, WT, NS>), dim3((unsigned)(tiles * a.c.kv_heads * a.psplits)),
+                     dim3(W::THREADS), 0, stream, a);
   return hipGetLastError();
 }
 
+template <int DP, int CT>
+hipError_t prefix_rows(const KvAttnArgs& a, hipStream_t stream) {
+  if constexpr (DP > 128) return prefix_as<DP, CT, 4, 1, 1>(a, stream);
+  else if (a.wide > 128) return prefix_as<DP, CT, 8, 1, 2>(a, stream);
+  else return prefix_as<DP, CT, 4, 2, 1>(a, stream);
+}
+
 template <int CT>
-hipError_t prefix_of(const KvAttnArgs& a, hipStream_t stream) {
-  if (a.c.head_dim <= 64) return prefix_as<64, CT, 4, 2, 1>(a, stream);
-  if (a.c.head_dim <= 96) return prefix_as<96, CT, 4, 2, 1>(a, stream);
-  if (a.c.head_dim <= 128) return prefix_as<128, CT, 4, 2, 1>(a, stream);
-  return prefix_as<256, CT, 4, 2, 1>(a, stream);
+hipError_t prefix_type(const KvAttnArgs& a, hipStream_t stream) {
+  if (a.c.head_dim <= 64) return prefix_rows<64, CT>(a, stream);
+  if (a.c.head_dim <= 96) return prefix_rows<96, CT>(a, stream);
+  if (a.c.head_dim <= 128) return prefix_rows<128, CT>(a, stream);
+  return prefix_rows<256, CT>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_kv_prefix(const KvAttnArgs& a, hipStream_t stream) {
-  if (a.c.type == kCacheInt8) return prefix_of<kCacheInt8>(a, stream);
-  if (a.c.type == kCacheE4m3) return prefix_of<kCacheE4m3>(a, stream);
-  return prefix_of<kCacheBf16>(a, stream);
+  if (a.c.type == kCacheInt8) return prefix_type<kCacheInt8>(a, stream);
+  if (a.c.type == kCacheE4m3) return prefix_type<kCacheE4m3>(a, stream);
+  return prefix_type<kCacheBf16>(a, stream);
 }
 
 }  // namespace qlora

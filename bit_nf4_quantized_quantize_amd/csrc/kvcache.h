@@ -52,7 +52,7 @@ struct KvAttnArgs {
   int64_t q_stride, S, table_cols, prefix_cols;
   int q_heads, splits, psplits;
   int waves, pwaves;  // per workgroup, set by the launcher
-  bool wide;          // the prefix in wide workgroups, set by the launcher
+  int wide;           // rows of a wide workgroup for the prefix, 0: narrow ones; set by the launcher
   float scale;
 };
 // The parts of a call without and with a shared prefix.

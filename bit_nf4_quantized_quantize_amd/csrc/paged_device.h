@@ -25,6 +25,22 @@ __device__ __forceinline__ Cut cut_of(int64_t n, int splits, int waves) {
   return c;
 }
 
+// The same where tiles are counted in 32 bits (n < 2^31), a fraction of the
+// instructions.
+struct Cut32 {
+  uint32_t tiles, per, parts;
+};
+__device__ __forceinline__ Cut32 cut32_of(uint32_t n, int splits, int waves) {
+  Cut32 c;
+  c.tiles = (n + kTile - 1) / kTile;
+  uint32_t most = (c.tiles + waves * kMinTiles - 1) / (uint32_t)(waves * kMinTiles);
+  if (most > (uint32_t)splits) most = splits;
+  if (most < 1) most = 1;
+  c.per = (c.tiles + most - 1) / most;
+  c.parts = c.per ? (c.tiles + c.per - 1) / c.per : 0;
+  return c;
+}
+
 // Keeps a wave's LDS accesses before and after it in program order for the
 // compiler; the LDS itself serves a wave's accesses in order.
 __device__ __forceinline__ void lds_in_order() {
@@ -66,13 +82,16 @@ __device__ __forceinline__ void split(const float (&p)[8], bf16x8 (&part)[3]) {
 }
 
 // The same in two parts: the second is rounded, so 16 bits stay at least (2^-8 of
-// a remainder under 2^-7).
+// a remainder under 2^-7).  INF: as above, no part is zero where the weight is not;
+// else the first is the weight cut off.
+template <bool INF>
 __device__ __forceinline__ void split2(const float (&p)[8], bf16x8 (&part)[2]) {
   uint32_t w[8];
   float left[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    w[j] = __builtin_elementwise_sub_sat(__float_as_uint(p[j]), 1u) & 0xFFFF0000u;
+    w[j] = INF ? __builtin_elementwise_sub_sat(__float_as_uint(p[j]), 1u) : __float_as_uint(p[j]);
+    w[j] &= 0xFFFF0000u;
     left[j] = p[j] - __uint_as_float(w[j]);
   }
   part[0] = upper(w);

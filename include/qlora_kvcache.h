@@ -116,7 +116,8 @@ int qlora_kv_attention(const void* q, int64_t q_stride, int64_t S, int32_t q_hea
  *
  *   prefix_table  int32 [prefix_cols]: the pages of the prefix; prefix_len int32
  *              [1] (device), cut to 0 .. prefix_cols * page_size.  Any length:
- *              the last page need not be full.
+ *              the last page need not be full.  prefix_cols * page_size at most
+ *              2^31 - 4097.
  *   table, lengths   the sequences' own tokens, as for qlora_paged_attention (a
  *              length of 0: the prefix alone); table_cols may be 0.
  *   the rest   as for qlora_paged_attention.

@@ -5,10 +5,11 @@ Tolerance.  The oracle takes the numbers that the codes stand for.  A score is a
 sum of at most 256 exact products in fp32, each addition off by at most a whole
 step (2 u, u = 2^-24), times a scale of its row and of the softmax: off by e = 2
 (d + 8) u |scale| sum |q_i k_i|, its weight by a relative e plus 16 u of the
-exponential and of the size of the score.  A weight enters the products with all
-its bits and is rounded once with the value's scale; n terms are added and parts
-joined, (2 n + 256) u.  With W = sum p_i |v_i|
-    |err| <= (2 e + (2 n + 256) u) W + 2^-8 |out| + n 2^-126 max |v|,
+exponential and of the size of the score.  A weight is rounded once with the
+value's scale and enters the products with all its bits, over a prefix of more
+than 32 rows with at least 16 (2^-16); n terms are added and parts joined, (2 n +
+256) u.  With W = sum p_i |v_i|
+    |err| <= (2^-16 + 2 e + (2 n + 256) u) W + 2^-8 |out| + n 2^-126 max |v|,
 the second for the rounding of the output to bfloat16, the third for weights that
 are no normal fp32 numbers: exp of a score 88 or more below the row's largest is
 under 2^-126 of the largest weight, which is 1 and part of the sum, and may count
@@ -88,7 +89,7 @@ def _check(K, q, cache, table, lengths, ptable=None, plen=0, scale=None, values=
     qsum = np.abs(_n(q)).sum(-1)
     e = 2 * (d + 8) * U * abs(sc) * qsum * kmax + 16 * U * (1 + abs(sc) * qsum * kmax)
     vmax = float(np.abs(values[1][np.isfinite(values[1])]).max())
-    tol = (2 * e[..., None] + (2 * n + 256) * U) * wt + 2.0 ** -8 * np.abs(ref) + n * 2.0 ** -126 * vmax
+    tol = (2.0 ** -16 + 2 * e[..., None] + (2 * n + 256) * U) * wt + 2.0 ** -8 * np.abs(ref) + n * 2.0 ** -126 * vmax
     err = np.abs(_n(out) - ref)
     assert (err <= tol).all(), (float((err - tol).max()), float(err.max()), page)
     got, none = _n(lse), np.isneginf(rlse)

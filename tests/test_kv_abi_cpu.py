@@ -134,7 +134,7 @@ def test_attention_refusals(name, order):
     assert f(S=0, q=None, out=None, lengths=None, table=None, **({"plen": None, "ptable": None} if "plen" in order
                                                                  else {})) == OK
     if "plen" in order:
-        assert f(pcols=-1) == BAD and f(pcols=2 ** 27) == BAD
+        assert f(pcols=-1) == BAD and f(pcols=2 ** 27) == BAD and f(pcols=2 ** 27 - 1) == BAD
         assert f(plen=None) == BAD and f(plen=MIS4) == AL and f(ptable=None) == BAD and f(ptable=MIS4) == AL
 
 

@@ -24,8 +24,9 @@ linears. That form also takes what the plain one lacks: rotary positions
 (qlora_rope), norms behind the branches, gates and a residual scale
     h = x + c * t1 * post1(L_o(...)),  y = h + c * t2 * post2(L_down(...)),
 gradients for the norm gains and gates that require them, and decoding from
-a paged key-value cache (prefill, decode). The attention core and SiLU stay
-fp32 torch ops. Blocks of this form may run on several streams at once, and
+a paged key-value cache (prefill, decode), which may hold its rows in 8 bits and
+a prefix that all sequences share (prefill_shared). The attention core and SiLU
+stay fp32 torch ops. Blocks of this form may run on several streams at once, and
 their forward be captured into a graph (prefill and decode not: the cache takes
 counts from the host); the plain one shares the binding's workspace of the
 device, so its calls belong on one stream.
@@ -39,6 +40,7 @@ from torch.autograd.function import once_differentiable
 
 from . import binding as B
 from . import decoder as D
+from . import kvcache as K
 
 LINEARS = ("q", "k", "v", "o", "gate", "up", "down")
 EPS = 1e-6
@@ -176,36 +178,64 @@ def rope(q, k, table, positions):
 
 class PagedCache:
     """The paged key-value cache of one block for up to `max_seqs` sequences of
-    up to `max_len` tokens: bfloat16 pages [num_pages, heads, page_size,
-    head_dim] of keys and values, the block table, and the pages not in use.
+    up to `max_len` tokens: pages [num_pages, heads, page_size, head_dim] of keys
+    and values, the block table, and the pages not in use. dtype is bfloat16, or
+    int8 or float8_e4m3fn for rows of codes with a scale each (`rows` is the
+    KVCache). With max_prefix the sequences may share up to that many tokens, which
+    come before their own and lie in pages of their own, once.
     The lengths are known to the host too, so running out of room raises
     before anything is enqueued.  page_size is a power of two from 16 to 1024,
-    head_dim a multiple of 8 up to 256, as the attention takes them, max_seqs at
-    most 4096, as the plan does."""
+    head_dim a multiple of 8 (of 16 for codes) up to 256, as the attention takes
+    them, max_seqs at most 4096, as the plan does."""
 
-    def __init__(self, num_pages, page_size, heads, head_dim, max_seqs, max_len, device=None):
+    def __init__(self, num_pages, page_size, heads, head_dim, max_seqs, max_len, device=None, dtype=torch.bfloat16,
+                 max_prefix=0):
         dev = device if device is not None else torch.device("cuda", torch.cuda.current_device())
-        if page_size not in (16, 32, 64, 128, 256, 512, 1024) or head_dim % 8 or not 8 <= head_dim <= 256:
-            raise ValueError("page_size must be a power of two in [16, 1024], head_dim a multiple of 8 in [8, 256]")
+        if dtype not in K.CACHE_TYPES:
+            raise ValueError("a cache is bfloat16, int8 or float8_e4m3fn")
+        unit = 8 if dtype == torch.bfloat16 else 16
+        if page_size not in (16, 32, 64, 128, 256, 512, 1024) or head_dim % unit or not unit <= head_dim <= 256:
+            raise ValueError(f"page_size must be a power of two in [16, 1024], head_dim a multiple of {unit} in [{unit}, "
+                             "256]")
         if not 1 <= max_seqs <= D.PLAN_MAX_SEQS or heads < 1:
             raise ValueError(f"max_seqs must be in [1, {D.PLAN_MAX_SEQS}], heads at least 1")
         if not 1 <= num_pages * page_size < 2 ** 31 or not 1 <= max_len <= 2 ** 31 - page_size:
             raise ValueError("num_pages and max_len must be at least 1, num_pages * page_size and max_len in whole pages "
                              "below 2^31")
-        shape = (num_pages, heads, page_size, head_dim)
-        self.k = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
-        self.v = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
-        self.page_size, self.max_len = int(page_size), int(max_len)
+        if not 0 <= max_prefix <= 2 ** 31 - 4097 - page_size or max_prefix + max_len > 2 ** 31 - page_size:
+            raise ValueError("max_prefix must be at least 0, max_prefix + max_len in whole pages below 2^31")
+        self.rows = K.KVCache.zeros(num_pages, heads, page_size, head_dim, dtype, dev)
+        self.k, self.v = self.rows.k, self.rows.v
+        self.page_size, self.max_len, self.max_prefix = int(page_size), int(max_len), int(max_prefix)
         self.free = torch.arange(num_pages, dtype=torch.int32, device=dev)
         self.table = torch.full((max_seqs, -(-self.max_len // page_size)), -1, dtype=torch.int32, device=dev)
         self.lens = torch.zeros(max_seqs, dtype=torch.int32, device=dev)
         self.host_lens = [0] * max_seqs
+        self.prefix_table = torch.full((-(-self.max_prefix // page_size),), -1, dtype=torch.int32, device=dev)
+        self.prefix_len = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.prefix_slots = torch.zeros(0, dtype=torch.int32, device=dev)
+        self.host_prefix = 0
         self.used = 0
+
+    def state(self):
+        """What the cache counts; set_state takes it back to that."""
+        return self.lens, self.host_lens, self.prefix_len, self.prefix_slots, self.host_prefix, self.used
+
+    def set_state(self, state):
+        self.lens, self.host_lens, self.prefix_len, self.prefix_slots, self.host_prefix, self.used = state
+
+    def _take(self, need):
+        """Refuses what cannot be had before anything is enqueued."""
+        if self.used + need > self.free.numel():
+            raise ValueError(f"{need} pages needed, {self.free.numel() - self.used} left")
+        if self.lens.is_cuda and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("PagedCache.add cannot be captured into a graph: its counts come from the host")
 
     def add(self, new_lens):
         """Room for new_lens[s] more tokens of each sequence: the PagedPlan of
-        their rows, in order of the sequences. The counts are copied from the host,
-        so a graph cannot hold this call (or prefill and decode, which make it)."""
+        their rows, in order of the sequences (positions count from the end of the
+        prefix). The counts are copied from the host, so a graph cannot hold this
+        call (or prefill and decode, which make it)."""
         if len(new_lens) != len(self.host_lens) or any(n < 0 for n in new_lens):
             raise ValueError(f"new_lens must be {len(self.host_lens)} counts")
         total = [c + n for c, n in zip(self.host_lens, new_lens)]
@@ -213,13 +243,27 @@ class PagedCache:
             raise ValueError(f"a sequence would pass max_len = {self.max_len} tokens")
         p = self.page_size
         need = sum(-(-t // p) - -(-c // p) for t, c in zip(total, self.host_lens))
-        if self.used + need > self.free.numel():
-            raise ValueError(f"{need} pages needed, {self.free.numel() - self.used} left")
-        if self.lens.is_cuda and torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("PagedCache.add cannot be captured into a graph: its counts come from the host")
+        self._take(need)
         new = torch.tensor(new_lens, dtype=torch.int32).to(self.lens.device)
         plan = D.qlora_paged_plan(self.lens, new, self.free[self.used:], self.table, p, sum(new_lens))
         self.lens, self.host_lens, self.used = plan.total_lens, total, self.used + need
+        return plan
+
+    def add_prefix(self, n):
+        """Room for a prefix of n tokens, before any others: the PagedPlan of its
+        rows."""
+        if self.host_prefix or any(self.host_lens):
+            raise ValueError("a prefix comes once, before the sequences' own tokens")
+        if not 1 <= n <= self.max_prefix:
+            raise ValueError(f"a prefix must have 1 to max_prefix = {self.max_prefix} tokens")
+        need = -(-n // self.page_size)
+        self._take(need)
+        dev = self.lens.device
+        plan = D.qlora_paged_plan(torch.zeros(1, dtype=torch.int32, device=dev),
+                                  torch.tensor([n], dtype=torch.int32).to(dev), self.free[self.used:],
+                                  self.prefix_table[None], self.page_size, n)
+        self.prefix_len, self.prefix_slots, self.host_prefix = plan.total_lens, plan.slots, int(n)
+        self.used += need
         return plan
 
 
@@ -227,9 +271,10 @@ def rms_norm(z, g):
     return z * torch.rsqrt(torch.mean(z * z, dim=-1, keepdim=True) + EPS) * g
 
 
-def causal_attention(q, k, v, heads):
+def causal_attention(q, k, v, heads, prefix=None):
     """softmax(q k^T / sqrt(d)) v per sequence and head, causal; fp32.
-    q, k, v: [batch, seq, hidden]."""
+    q, k, v: [batch, seq, hidden]. prefix: keys and values [tokens, heads, d]
+    that come before every sequence."""
     b, t, hd = q.shape
     d = hd // heads
 
@@ -239,8 +284,15 @@ def causal_attention(q, k, v, heads):
     qh, kh, vh = split(q), split(k), split(v)
     scores = torch.matmul(qh, kh.transpose(-1, -2).contiguous()) / math.sqrt(d)
     future = torch.triu(torch.ones(t, t, dtype=torch.bool, device=q.device), diagonal=1)
-    p = torch.softmax(scores.masked_fill(future, float("-inf")), dim=-1)
-    return torch.matmul(p, vh).permute(0, 2, 1, 3).reshape(b, t, hd)
+    scores = scores.masked_fill(future, float("-inf"))
+    if prefix is None:
+        return torch.matmul(torch.softmax(scores, dim=-1), vh).permute(0, 2, 1, 3).reshape(b, t, hd)
+    pk, pv = (z.float().transpose(0, 1).contiguous() for z in prefix)
+    before = torch.matmul(qh, pk.transpose(-1, -2).contiguous()) / math.sqrt(d)
+    p = torch.softmax(torch.cat((before, scores), -1), dim=-1)
+    n = pk.shape[1]
+    o = torch.matmul(p[..., :n].contiguous(), pv) + torch.matmul(p[..., n:].contiguous(), vh)
+    return o.permute(0, 2, 1, 3).reshape(b, t, hd)
 
 
 class QLoraBlock:
@@ -305,10 +357,10 @@ class QLoraBlock:
 
         return self._fused(x, attend)
 
-    def cache(self, num_pages, page_size, max_seqs, max_len):
+    def cache(self, num_pages, page_size, max_seqs, max_len, dtype=torch.bfloat16, max_prefix=0):
         """A PagedCache for this block."""
         return PagedCache(num_pages, page_size, self.heads, self.hidden // self.heads, max_seqs, max_len,
-                          self.lin["q"].A.device)
+                          self.lin["q"].A.device, dtype, max_prefix)
 
     def _check_cached(self, x, cache):
         """What a cached call needs of x, the cache and the rotary table."""
@@ -322,22 +374,47 @@ class QLoraBlock:
         if self.rope is not None and (self.rope.rot_dim > d or self.rope.turns.device != cache.k.device):
             raise ValueError(f"the rotary table must be of at most {d} elements and on the cache's device")
 
-    def _cached(self, x, cache, new_lens, attend):
-        """_fused on the rows of a plan for new_lens more tokens, attend(plan, q, k,
-        v).  If that fails the cache counts the tokens it had before: what was
-        stored lies behind them and is not used."""
-        before = cache.lens, cache.host_lens, cache.used
-        plan = cache.add(new_lens)
+    def _cached(self, x, cache, add, attend):
+        """_fused on the rows of the plan that add() makes, attend(plan, q, k, v).
+        If that fails the cache counts the tokens it had before: what was stored
+        lies behind them and is not used."""
+        before = cache.state()
+        plan = add()
         try:
             return self._fused(x, lambda q, k, v: attend(plan, q, k, v))
         except BaseException:
-            cache.lens, cache.host_lens, cache.used = before
+            cache.set_state(before)
             raise
+
+    def _prompt(self, x, cache, positions, slots, q, k, v, prefix=None):
+        """The attention of prompts x [batch, seq, hidden], causal and behind the
+        prefix, with their keys and values stored."""
+        b, t, _ = x.shape
+        if self.rope is not None:
+            q, k = D.qlora_rope(q, k, self.rope, positions)
+        K.qlora_kv_write(None, k, v, None, None, slots, cache.rows)
+        q, k, v = (z.float().view(b, t, self.hidden) for z in (q, k, v))
+        return causal_attention(q, k, v, self.heads, prefix).reshape(b * t, self.hidden).to(torch.bfloat16)
+
+    @torch.no_grad()
+    def prefill_shared(self, x, cache):
+        """The tokens x [seq, hidden] that all sequences of the cache share, before
+        any of their own: the block's output, with their keys and values stored
+        once."""
+        self._check_cached(x, cache)
+        if x.dim() != 2 or x.shape[1] != self.hidden:
+            raise ValueError(f"prefill_shared needs x [seq, {self.hidden}]")
+
+        def attend(plan, q, k, v):
+            return self._prompt(x[None], cache, plan.positions, plan.slots, q, k, v)
+
+        return self._cached(x, cache, lambda: cache.add_prefix(x.shape[0]), attend)
 
     @torch.no_grad()
     def prefill(self, x, cache):
         """The first tokens x [batch, seq, hidden] of the cache's sequences 0 ..
-        batch - 1: the block's output, with their keys and values stored."""
+        batch - 1, behind the prefix if there is one: the block's output, with their
+        keys and values stored."""
         self._check_cached(x, cache)
         if x.dim() != 3 or x.shape[2] != self.hidden or x.shape[0] > len(cache.host_lens) or any(cache.host_lens):
             raise ValueError(f"prefill needs x [batch, seq, {self.hidden}] and an empty cache of at least batch "
@@ -345,13 +422,18 @@ class QLoraBlock:
         b, t, _ = x.shape
 
         def attend(plan, q, k, v):
-            if self.rope is not None:
-                q, k = D.qlora_rope(q, k, self.rope, plan.positions)
-            D.qlora_rope_cache_write(None, k, v, None, None, plan.slots, cache.k, cache.v)
-            q, k, v = (z.float().view(b, t, self.hidden) for z in (q, k, v))
-            return causal_attention(q, k, v, self.heads).reshape(b * t, self.hidden).to(torch.bfloat16)
+            prefix = None
+            if cache.host_prefix:
+                prefix = K.qlora_kv_read(cache.rows, cache.prefix_slots, dtype=torch.float32)
+            return self._prompt(x, cache, self._behind(plan.positions, cache), plan.slots, q, k, v, prefix)
 
-        return self._cached(x, cache, [t if s < b else 0 for s in range(len(cache.host_lens))], attend)
+        new_lens = [t if s < b else 0 for s in range(len(cache.host_lens))]
+        return self._cached(x, cache, lambda: cache.add(new_lens), attend)
+
+    @staticmethod
+    def _behind(positions, cache):
+        """Positions counted from the prefix's first token."""
+        return positions + cache.host_prefix if cache.host_prefix else positions
 
     @torch.no_grad()
     def decode(self, x, cache):
@@ -363,10 +445,16 @@ class QLoraBlock:
             raise ValueError(f"decode needs x [{S}, {self.hidden}]")
 
         def attend(plan, q, k, v):
-            q = D.qlora_rope_cache_write(q, k, v, self.rope, plan.positions, plan.slots, cache.k, cache.v)
-            return D.qlora_paged_attention(q, cache.k, cache.v, cache.table, cache.lens).view(S, self.hidden)
+            q = K.qlora_kv_write(q, k, v, self.rope, self._behind(plan.positions, cache), plan.slots, cache.rows)
+            if cache.host_prefix:
+                o = K.qlora_prefix_attention(q, cache.rows, cache.prefix_table, cache.prefix_len, cache.table, cache.lens)
+            elif cache.rows.k_scale is not None:
+                o = K.qlora_kv_attention(q, cache.rows, cache.table, cache.lens)
+            else:
+                o = D.qlora_paged_attention(q, cache.k, cache.v, cache.table, cache.lens)
+            return o.view(S, self.hidden)
 
-        return self._cached(x, cache, [1] * S, attend)
+        return self._cached(x, cache, lambda: cache.add([1] * S), attend)
 
     def __call__(self, x, checkpoint=False):
         """x: fp32 [batch, seq, hidden] -> y (same shape)."""

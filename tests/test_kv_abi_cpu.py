@@ -247,3 +247,19 @@ def test_a_missing_module_is_reported(monkeypatch):
     f, kw = _calls()["read"]
     with pytest.raises(B.QLoraLibraryError, match="build it"):
         f(**kw)
+
+
+# ---------------------------------------------------------------- the block's cache
+
+@pytest.mark.parametrize("bad", [
+    dict(dtype=torch.float16), dict(dtype=torch.int8, head_dim=72), dict(dtype=torch.float8_e4m3fn, head_dim=8),
+    dict(max_prefix=-1), dict(max_prefix=2 ** 31), dict(max_prefix=2 ** 31 - 100, max_len=64)])
+def test_caches_that_the_block_does_not_make(bad, monkeypatch):
+    from bit_nf4_quantized_quantize_amd import block as BL
+    good = dict(num_pages=2, page_size=16, heads=2, head_dim=64, max_seqs=3, max_len=32, device="cpu")
+    for t in K.CACHE_TYPES:
+        c = BL.PagedCache(**good, dtype=t, max_prefix=20)
+        assert c.k.dtype == t and (c.rows.k_scale is None) == (t == torch.bfloat16) and c.prefix_table.shape == (2,)
+    monkeypatch.setattr(torch, "zeros", lambda *a, **k: pytest.fail("allocated"))
+    with pytest.raises(ValueError):
+        BL.PagedCache(**{**good, **bad})

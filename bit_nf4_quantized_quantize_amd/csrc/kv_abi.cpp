@@ -61,6 +61,9 @@ int check_attention(const qlora_kv_cache* c, int64_t S, int32_t q_heads, int64_t
   // positions in the prefix are counted a step or two ahead in 32 bits
   if (prefix_cols * c->page_size > kMaxRows - 4096)
     return fail(QLORA_ERR_INVALID_ARG, "%s: prefix_cols * page_size must be at most 2^31 - 4097", fn);
+  // a wave per row joins the parts: a grid holds 2^32 - 1 threads
+  if (prefix_cols && S * q_heads >= (1 << 26))
+    return fail(QLORA_ERR_INVALID_ARG, "%s: S * q_heads must be below 2^26 with a prefix", fn);
   return QLORA_OK;
 }
 

@@ -428,8 +428,20 @@ void attention_of(const KvAttnArgs& a, hipStream_t stream) {
   else attention_as<256, 4, CT>(a, stream);
 }
 
-int waves_for(int64_t groups, int head_dim, int64_t max_len) {
-  return groups * ((max_len + kTile - 1) / kTile) >= 128 * 256 && head_dim <= 128 ? 8 : 4;
+// Eight waves per workgroup for large calls, by what the table can hold (128 tiles
+// per CU), where fewer, longer streams read a little faster (8 sequences of 32768 to
+// 65536 in int8, 64 on 8 heads: 162 us with four, 155 with eight; 16 of 1 to 4096,
+// 32 heads in E4M3: 58 and 57), and for codes where one launch has fewer workgroups
+// than the card CUs (one of 512, 32 heads: 10.3 and 8.6); else four: in between the
+// waves run out of tiles (256 of 0 to 700 behind a prefix, 32 on 8 heads: 49 and
+// 62, two waves 51).  Heads of more than 128 keep four: eight waves' registers and V
+// tiles would leave a CU nothing else.
+int waves_for(const KvAttnArgs& a) {
+  if (a.psplits || a.c.head_dim > 128) return 4;
+  const int64_t group = a.q_heads / a.c.kv_heads, groups = a.S * a.c.kv_heads * ((group + 15) / 16);
+  const int64_t tiles = ((a.table_cols << a.c.page_shift) + kTile - 1) / kTile;
+  if (a.splits == 1 && a.c.type != kCacheBf16 && groups <= 256) return 8;
+  return groups * tiles >= 128 * 256 ? 8 : 4;
 }
 
 }  // namespace
@@ -459,7 +471,7 @@ KvParts kv_parts(const KvCache& c, int64_t S, int q_heads, int64_t table_cols, i
 hipError_t launch_kv_attention(const KvAttnArgs& args, hipStream_t stream) {
   KvAttnArgs a = args;
   const int64_t group = a.q_heads / a.c.kv_heads;
-  a.waves = a.psplits ? 4 : waves_for(a.S * a.c.kv_heads * ((group + 15) / 16), a.c.head_dim, a.table_cols << a.c.page_shift);
+  a.waves = waves_for(a);
   a.wide = a.psplits ? wide_rows(a.S * group, a.c.head_dim) : 0;
   a.pwaves = a.wide ? kWideWaves : a.waves;
   if (a.wide) {
@@ -469,8 +481,7 @@ hipError_t launch_kv_attention(const KvAttnArgs& args, hipStream_t stream) {
   if (a.c.type == kCacheInt8) attention_of<kCacheInt8>(a, stream);
   else if (a.c.type == kCacheE4m3) attention_of<kCacheE4m3>(a, stream);
   else attention_of<kCacheBf16>(a, stream);
-  if (a.psplits + a.splits > 1)
-  {
+  if (a.psplits + a.splits > 1) {
     // a wave per row once the rows fill the card (4096 rows of 9 parts: 7.0 us, with
     // four waves 12.6; 512 rows of 16: 9.5 and 4.2)
     const int64_t rows = a.S * a.q_heads;

@@ -120,7 +120,7 @@ int qlora_kv_attention(const void* q, int64_t q_stride, int64_t S, int32_t q_hea
  *              2^31 - 4097.
  *   table, lengths   the sequences' own tokens, as for qlora_paged_attention (a
  *              length of 0: the prefix alone); table_cols may be 0.
- *   the rest   as for qlora_paged_attention.
+ *   the rest   as for qlora_paged_attention.  S * q_heads < 2^26.
  * Tokens of a page that is negative or not below num_pages take no part; a
  * sequence in which no token takes part gives zeros (lse -inf).  Results repeat
  * bit for bit.

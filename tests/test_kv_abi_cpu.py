@@ -135,6 +135,7 @@ def test_attention_refusals(name, order):
                                                                  else {})) == OK
     if "plen" in order:
         assert f(pcols=-1) == BAD and f(pcols=2 ** 27) == BAD and f(pcols=2 ** 27 - 1) == BAD
+        assert f(S=2 ** 15, q_heads=2048, q_stride=2 ** 20) == BAD
         assert f(plen=None) == BAD and f(plen=MIS4) == AL and f(ptable=None) == BAD and f(ptable=MIS4) == AL
 
 

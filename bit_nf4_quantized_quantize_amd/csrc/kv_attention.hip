@@ -129,7 +129,7 @@ __device__ __forceinline__ void place_of(const Columns& c, int col, int64_t* s, 
 // the sequences' kv heads, tiles of heads and parts, all in x; else those in x and
 // the sequences in y.
 template <int DP, int W, int CT>
-__global__ __launch_bounds__(64 * W, 2) void kv_attention_kernel(KvAttnArgs a, int qtiles, int ptiles) {
+__global__ __launch_bounds__(64 * W, DP > 128 ? 1 : 2) void kv_attention_kernel(KvAttnArgs a, int qtiles, int ptiles) {
   using Tile = KvTile<DP, CT>;
   constexpr int CH = DP / Tile::EV;
   constexpr int PITCH = DP + 16;  // of the V tile: 16 rows of one column go to different banks

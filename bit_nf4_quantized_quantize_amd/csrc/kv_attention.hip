@@ -1,6 +1,25 @@
 // Attention of one new token per sequence over a paged cache of any type, and
 // over a prefix that the sequences share, gfx950 (definitions in
 // include/qlora_kvcache.h).
+//
+// The narrow workgroups below are those of the bfloat16 cache's attention: the
+// query heads of a kv head are the 16 columns of the products, a wave works alone
+// on tiles of 32 tokens with a running maximum and sum, weights enter the product
+// with V as three bfloat16 parts with all of their 24 bits, long lengths are cut
+// and joined.  Over a prefix the columns are heads of any sequences, so its keys
+// are read once for 16 rows.  Codes are read 16 bytes per lane and made bfloat16
+// numbers, exactly, where they enter the products (E4M3: one instruction for two;
+// whole numbers: three); a key's scale is put on its score and a value's on its
+// weight in fp32, four of each per lane and tile.
+// Bound by HBM, at half the bytes per token of bfloat16, so at twice the work per
+// byte: 8 sequences of 32768 to 65536 tokens, 64 on 8 heads of 128, in int8 155-159
+// us (830 MB, 5.3 TB/s; a streaming read reaches 5.6); 16 of 1 to 4096, 32 heads, in
+// E4M3 57-60 us and 4 to 5 for the join (277 MB); one of 512, 32 heads, in int8 8.6
+// us; 16 sequences behind 8191 shared tokens, 32 heads, bf16, 41 us (201 MB) and 5.
+// Short own lengths behind a prefix are further off: 256 of 0 to 700, 32 on 8
+// heads, E4M3, 50 us (189 MB take 34; 45 with even lengths), the first loads of a
+// workgroup and its end being half of its life.  Not kept: Q in LDS (164 registers
+// as before), registers for four waves per SIMD (spills, 57 -> 87 us).
 #include <type_traits>
 
 #include "device.h"
@@ -450,6 +469,10 @@ int waves_for(const KvAttnArgs& a) {
 static int wide_rows(int64_t rows, int head_dim) { return rows <= 32 ? 0 : rows <= 128 || head_dim > 128 ? 128 : 256; }
 constexpr int kWideWaves = 2;  // a part of the prefix has the tiles of that many narrow waves at least
 
+// The own tokens' parts as without a prefix (finer ones, for the join that is there
+// anyway, do not pay: 256 sequences of 0 to 700 in parts of 256 tokens 52 us, whole
+// 50).  The prefix's: a workgroup per CU, as far as its length gives each some
+// tiles (16 rows of 8191 tokens, 32 heads: 41 us so, 45 with two, 49 with four).
 KvParts kv_parts(const KvCache& c, int64_t S, int q_heads, int64_t table_cols, int64_t prefix_cols) {
   KvParts p;
   const int64_t max_len = table_cols << c.page_shift;
@@ -459,7 +482,7 @@ KvParts kv_parts(const KvCache& c, int64_t S, int q_heads, int64_t table_cols, i
   const int64_t rows = S * (q_heads / c.kv_heads), cap = prefix_cols << c.page_shift;
   const int wide = wide_rows(rows, c.head_dim);
   const int64_t groups = c.kv_heads * (wide ? (rows + wide - 1) / wide : (rows + 15) / 16);
-  int64_t n = ((wide ? 1 : 2) * 256 + groups - 1) / groups;
+  int64_t n = (256 + groups - 1) / groups;
   const int64_t least = (wide ? kWideWaves : 4) * kMinTiles * kTile, most = (cap + least - 1) / least;
   if (n > most) n = most;
   if (n > kMaxParts / 2) n = kMaxParts / 2;

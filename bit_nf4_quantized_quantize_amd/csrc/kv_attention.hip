@@ -18,7 +18,9 @@
 // us; 16 sequences behind 8191 shared tokens, 32 heads, bf16, 41 us (201 MB) and 5.
 // Short own lengths behind a prefix are further off: 256 of 0 to 700, 32 on 8
 // heads, E4M3, 50 us (189 MB take 34; 45 with even lengths), the first loads of a
-// workgroup and its end being half of its life.  Not kept: Q in LDS (164 registers
+// workgroup and its end being half of its life.  Behind a prefix of many rows these
+// workgroups, the last to touch a row, also join its parts: 55 us, where a kernel
+// for that took 11.  Not kept: Q in LDS (164 registers
 // as before), registers for four waves per SIMD (spills, 57 -> 87 us).
 #include <type_traits>
 
@@ -198,7 +200,7 @@ __global__ __launch_bounds__(64 * W, DP > 128 ? 1 : 2) void kv_attention_kernel(
     n = cut_length(a.lengths[cols.s], a.table_cols, kc.page_shift);
     cut = cut32_of((uint32_t)n, a.splits, W);
   }
-  if (parts > 1 && (uint32_t)z >= cut.parts) return;
+  if (parts > 1 && !a.joined && (uint32_t)z >= cut.parts) return;
   const int64_t first = (int64_t)z * cut.per;
   const int64_t last = first + cut.per < cut.tiles ? first + cut.per : cut.tiles;
 
@@ -333,6 +335,9 @@ __global__ __launch_bounds__(64 * W, DP > 128 ? 1 : 2) void kv_attention_kernel(
 #pragma unroll
   for (int i = 0; i < DP / 16; ++i) *reinterpret_cast<floatx4*>(ow + col * OP + 16 * i + 4 * g) = acc[i];
   __syncthreads();
+  uint32_t pre = 0;
+  if (a.joined)
+    pre = cut32_of((uint32_t)cut_length(*a.prefix_len, a.prefix_cols, kc.page_shift), a.psplits, a.pwaves).parts;
   for (int e = threadIdx.x; e < cols.n * (d / 4); e += 64 * W) {
     const int h = e / (d / 4), c = e % (d / 4) * 4;
     float mx = -INFINITY;
@@ -351,7 +356,23 @@ __global__ __launch_bounds__(64 * W, DP > 128 ? 1 : 2) void kv_attention_kernel(
     int head;
     place_of(cols, h, &s, &head);
     const int64_t row = s * a.q_heads + head;
-    if (parts > 1) {
+    if (a.joined) {  // the prefix's parts are there: this is the row's last one
+      const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row * parts;
+      const float* src = a.part_o + row * parts * d + c;
+      float all = mx;
+      for (uint32_t i = 0; i < pre; ++i) all = fmaxf(all, ml[i].x);
+      const float au = all == -INFINITY ? 0.0f : all, f = __builtin_amdgcn_exp2f(mx - au);
+      sum *= f, o *= f;
+#pragma unroll 8
+      for (uint32_t i = 0; i < pre; ++i) {
+        const float2 v = ml[i];
+        const float g2 = __builtin_amdgcn_exp2f(v.x - au);
+        sum += v.y * g2;
+        o += *reinterpret_cast<const floatx4*>(src + (int64_t)i * d) * g2;
+      }
+      mx = all;
+    }
+    if (parts > 1 && !a.joined) {
       const int64_t at = row * parts + (shared ? z : a.psplits + z);
       *reinterpret_cast<floatx4*>(a.part_o + at * d + c) = o;
       if (c == 0) a.part_ml[at * 2] = mx, a.part_ml[at * 2 + 1] = sum;
@@ -469,9 +490,10 @@ int waves_for(const KvAttnArgs& a) {
 static int wide_rows(int64_t rows, int head_dim) { return rows <= 32 ? 0 : rows <= 128 || head_dim > 128 ? 128 : 256; }
 constexpr int kWideWaves = 2;  // a part of the prefix has the tiles of that many narrow waves at least
 
-// The own tokens' parts as without a prefix (finer ones, for the join that is there
-// anyway, do not pay: 256 sequences of 0 to 700 in parts of 256 tokens 52 us, whole
-// 50).  The prefix's: a workgroup per CU, as far as its length gives each some
+// The own tokens' parts as without a prefix; whole behind one of many rows if there
+// are enough workgroups, which then join the prefix's parts (64 sequences of 100 to
+// 800, 64 on 8 heads: 26 us, against 23 and 11 for the join; finer parts, for the
+// join, do not pay: 256 of 0 to 700 in parts of 256 tokens 52 us, whole 50).  The prefix's: a workgroup per CU, as far as its length gives each some
 // tiles (16 rows of 8191 tokens, 32 heads: 41 us so, 45 with two, 49 with four).
 KvParts kv_parts(const KvCache& c, int64_t S, int q_heads, int64_t table_cols, int64_t prefix_cols) {
   KvParts p;
@@ -482,6 +504,7 @@ KvParts kv_parts(const KvCache& c, int64_t S, int q_heads, int64_t table_cols, i
   const int64_t rows = S * (q_heads / c.kv_heads), cap = prefix_cols << c.page_shift;
   const int wide = wide_rows(rows, c.head_dim);
   const int64_t groups = c.kv_heads * (wide ? (rows + wide - 1) / wide : (rows + 15) / 16);
+  if (wide && S * c.kv_heads * ((q_heads / c.kv_heads + 15) / 16) >= 256) p.own = 1;
   int64_t n = (256 + groups - 1) / groups;
   const int64_t least = (wide ? kWideWaves : 4) * kMinTiles * kTile, most = (cap + least - 1) / least;
   if (n > most) n = most;
@@ -497,6 +520,7 @@ hipError_t launch_kv_attention(const KvAttnArgs& args, hipStream_t stream) {
   a.waves = waves_for(a);
   a.wide = a.psplits ? wide_rows(a.S * group, a.c.head_dim) : 0;
   a.pwaves = a.wide ? kWideWaves : a.waves;
+  a.joined = a.wide && a.splits == 1;
   if (a.wide) {
     const hipError_t e = launch_kv_prefix(a, stream);
     if (e != hipSuccess) return e;
@@ -504,7 +528,7 @@ hipError_t launch_kv_attention(const KvAttnArgs& args, hipStream_t stream) {
   if (a.c.type == kCacheInt8) attention_of<kCacheInt8>(a, stream);
   else if (a.c.type == kCacheE4m3) attention_of<kCacheE4m3>(a, stream);
   else attention_of<kCacheBf16>(a, stream);
-  if (a.psplits + a.splits > 1) {
+  if (a.psplits + a.splits > 1 && !a.joined) {
     // a wave per row once the rows fill the card (4096 rows of 9 parts: 7.0 us, with
     // four waves 12.6; 512 rows of 16: 9.5 and 4.2)
     const int64_t rows = a.S * a.q_heads;

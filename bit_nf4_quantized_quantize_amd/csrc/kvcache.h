@@ -53,6 +53,7 @@ struct KvAttnArgs {
   int q_heads, splits, psplits;
   int waves, pwaves;  // per workgroup, set by the launcher
   int wide;           // rows of a wide workgroup for the prefix, 0: narrow ones; set by the launcher
+  bool joined;        // the own tokens' workgroups join the prefix's parts; set by the launcher
   float scale;
 };
 // The parts of a call without and with a shared prefix.

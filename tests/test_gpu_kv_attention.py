@@ -134,6 +134,8 @@ SHARED = [  # S, H, KV, d, page, cols, pcols, lengths (high), prefix
     (20, 8, 1, 256, 16, 2, 20, 31, 300),                    # 160 rows, heads of 256
     (12, 40, 2, 112, 16, 1, 40, 9, 640),                    # 240, twenty heads to one
     (3, 20, 1, 240, 32, 2, 30, 50, 950),
+    (130, 4, 2, 64, 16, 48, 10, 700, 150),                  # long own lengths of many sequences: joined where they end
+    (17, 12, 2, 64, 16, 64, 12, 1000, 190),                 # of few: cut, and joined by themselves
 ]
 
 

@@ -20,8 +20,8 @@
 // heads, E4M3, 50 us (189 MB take 34; 45 with even lengths), the first loads of a
 // workgroup and its end being half of its life.  Behind a prefix of many rows these
 // workgroups, the last to touch a row, also join its parts: 55 us, where a kernel
-// for that took 11.  Not kept: Q in LDS (164 registers
-// as before), registers for four waves per SIMD (spills, 57 -> 87 us).
+// for that took 11.  Not kept: Q in LDS (164 registers as before), registers for
+// four waves per SIMD (spills, 57 -> 87 us).
 #include <type_traits>
 
 #include "device.h"
@@ -31,7 +31,7 @@
 
 namespace qlora {
 
-// ------------------------------------------------- few rows: narrow workgroups
+// ------------------------------------------- few rows or tokens: narrow workgroups
 
 namespace {
 
@@ -486,15 +486,25 @@ int waves_for(const KvAttnArgs& a) {
 
 }  // namespace
 
-// Rows of a prefix's workgroup: narrow ones (0) up to 32.
-static int wide_rows(int64_t rows, int head_dim) { return rows <= 32 ? 0 : rows <= 128 || head_dim > 128 ? 128 : 256; }
+// Rows of a prefix's workgroup: narrow ones (0) up to 32, and as long as they read
+// little in all, in the launch of the own tokens instead of one before it (128 rows,
+// 8 kv heads, int8, 1000 tokens 19 us, wide 26; 4000, at the limit, 31 and 32; 8000
+// 46 and 36).  1024 rows at most, so that a grid holds them.  Wide ones of 128 up
+// to 256 rows (256 of 8 kv heads, 2000 tokens 31 us, with 256 34; 16000 56 and 59;
+// 512 of 16000 87 and 82).
+static int wide_rows(int64_t rows, const KvCache& c, int64_t prefix_cols) {
+  const int64_t reads = ((rows + 15) / 16) * c.kv_heads * (prefix_cols << c.page_shift);
+  if (rows <= 32 || (rows <= 1024 && reads <= 1 << 18)) return 0;
+  return rows <= 256 || c.head_dim > 128 ? 128 : 256;
+}
 constexpr int kWideWaves = 2;  // a part of the prefix has the tiles of that many narrow waves at least
 
 // The own tokens' parts as without a prefix; whole behind one of many rows if there
-// are enough workgroups, which then join the prefix's parts (64 sequences of 100 to
-// 800, 64 on 8 heads: 26 us, against 23 and 11 for the join; finer parts, for the
-// join, do not pay: 256 of 0 to 700 in parts of 256 tokens 52 us, whole 50).  The prefix's: a workgroup per CU, as far as its length gives each some
-// tiles (16 rows of 8191 tokens, 32 heads: 41 us so, 45 with two, 49 with four).
+// are enough workgroups, which then can join the prefix's parts (64 sequences of 100
+// to 800, 64 on 8 heads: 26 us, against 23 and 11 for the join; finer parts, for the
+// join, do not pay: 256 of 0 to 700 in parts of 256 tokens 52 us, whole 50).  The
+// prefix's: a workgroup per CU, as far as its length gives each some tiles (16 rows
+// of 8191 tokens, 32 heads: 41 us so, 45 with two, 49 with four).
 KvParts kv_parts(const KvCache& c, int64_t S, int q_heads, int64_t table_cols, int64_t prefix_cols) {
   KvParts p;
   const int64_t max_len = table_cols << c.page_shift;
@@ -502,7 +512,7 @@ KvParts kv_parts(const KvCache& c, int64_t S, int q_heads, int64_t table_cols, i
   p.prefix = 0;
   if (!prefix_cols || !S) return p;
   const int64_t rows = S * (q_heads / c.kv_heads), cap = prefix_cols << c.page_shift;
-  const int wide = wide_rows(rows, c.head_dim);
+  const int wide = wide_rows(rows, c, prefix_cols);
   const int64_t groups = c.kv_heads * (wide ? (rows + wide - 1) / wide : (rows + 15) / 16);
   if (wide && S * c.kv_heads * ((q_heads / c.kv_heads + 15) / 16) >= 256) p.own = 1;
   int64_t n = (256 + groups - 1) / groups;
@@ -518,9 +528,12 @@ hipError_t launch_kv_attention(const KvAttnArgs& args, hipStream_t stream) {
   KvAttnArgs a = args;
   const int64_t group = a.q_heads / a.c.kv_heads;
   a.waves = waves_for(a);
-  a.wide = a.psplits ? wide_rows(a.S * group, a.c.head_dim) : 0;
+  a.wide = a.psplits ? wide_rows(a.S * group, a.c, a.prefix_cols) : 0;
   a.pwaves = a.wide ? kWideWaves : a.waves;
-  a.joined = a.wide && a.splits == 1;
+  // A workgroup of one row would join it with a few of its threads only (behind 2000
+  // tokens, bf16, 256 sequences on 32 of 32 heads: joined 144 us, by the kernel below
+  // 115; 128 on 8 of 32: 43 and 46).
+  a.joined = a.wide && a.splits == 1 && group > 1;
   if (a.wide) {
     const hipError_t e = launch_kv_prefix(a, stream);
     if (e != hipSuccess) return e;

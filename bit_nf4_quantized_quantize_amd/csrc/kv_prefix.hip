@@ -1,6 +1,6 @@
 // Attention over a shared prefix for many query rows, gfx950: the prefix's part
 // of qlora_prefix_attention (include/qlora_kvcache.h) when the rows of a kv head
-// (sequences times heads that share it) are more than a narrow workgroup takes.
+// (sequences times heads that share it) and the prefix's tokens are many.
 #include <type_traits>
 
 #include "device.h"
@@ -36,7 +36,7 @@ namespace {
 // missing tokens 4.  Scores, weights and output of a tile in one block: 73 us.
 // 256 rows per workgroup (K and V made bfloat16 and read from memory half as
 // often): 66 us where 128 take 73, but twice the parts to join (10.8 us, 7.1); up to
-// 128 rows two waves share a row's tokens instead.  1024 rows behind 2000 tokens,
+// 256 rows workgroups of 128, two waves of which share a row's tokens.  1024 rows behind 2000 tokens,
 // 32 on 8 heads, E4M3: 27 us.
 template <int DP, int CT, int WQ, int WT, int NS>
 struct Wide {

@@ -24,20 +24,22 @@ namespace {
 // its part of the output in block i + 1; within a block nothing depends on
 // anything but the last ones' results.
 //
-// A weight enters the product with V as two bfloat16 parts, so with 16 bits, 2^-17
-// of it at most lost where the output is rounded by 2^-9: here the products set the
-// time, a third part would add a fourth to them.
+// A weight enters the product with V as three bfloat16 parts, with all of its 24
+// bits, as in the narrow workgroups: a row's result does not depend on which of them
+// take it.  Two parts (64 sequences behind 16384 tokens, as below: 64 us where three
+// take 77) left 0.45 % of the results not the nearest bfloat16 number, three 0.04 %.
 //
 // Bound by the products and the softmax between them: 64 sequences of 8 heads each
-// on 8 kv heads of 128 behind 16384 tokens in int8 64 us, 51.6 GFLOP with both
-// parts, 0.8 PFLOP/s (a large library product reaches 1.19).  Of that the matrix
-// instructions alone take 25 us, the launch, first loads and the 33 MB of parts 10,
-// LDS reads 5, exponentials and parts 6, codes to bfloat16 1 to 6, maxima and
-// missing tokens 4.  Scores, weights and output of a tile in one block: 73 us.
-// 256 rows per workgroup (K and V made bfloat16 and read from memory half as
-// often): 66 us where 128 take 73, but twice the parts to join (10.8 us, 7.1); up to
-// 256 rows workgroups of 128, two waves of which share a row's tokens.  1024 rows behind 2000 tokens,
-// 32 on 8 heads, E4M3: 27 us.
+// on 8 kv heads of 128 behind 16384 tokens in int8 77 us, 68.7 GFLOP with all
+// parts, 0.9 PFLOP/s (a large library product reaches 1.19).  1024 rows behind 2000
+// tokens, 32 on 8 heads, E4M3: 31 us.
+// The rest was measured with two parts.  Of 64 us the matrix instructions alone took
+// 25, the launch, first loads and the 33 MB of parts 10, LDS reads 5, exponentials
+// and parts 6, codes to bfloat16 1 to 6, maxima and missing tokens 4.  Scores,
+// weights and output of a tile in one block: 73 us.  256 rows per workgroup (K and V
+// made bfloat16 and read from memory half as often): 66 us where 128 took 73, but
+// twice the parts to join (10.8 us, 7.1); up to 256 rows workgroups of 128, two
+// waves of which share a row's tokens.
 template <int DP, int CT, int WQ, int WT, int NS>
 struct Wide {
   static constexpr int THREADS = 64 * WQ * WT;
@@ -186,7 +188,7 @@ __global__ __launch_bounds__(64 * WQ * WT) void kv_prefix_kernel(KvAttnArgs a) {
 #pragma unroll
     for (int j = 0; j < 16; ++j) acc[t][j] = 0.0f;
   float x[16];            // scores of the tile less m, in base 2
-  bf16x8 part[2][2] = {};  // weights of the tile before it: steps of 16 tokens, parts
+  bf16x8 part[2][3] = {};  // weights of the tile before it: steps of 16 tokens, parts
 
   // A tile's scores less m, and the largest
   auto scores = [&](const floatx16& sc, const float* ks, float* top) {
@@ -234,7 +236,7 @@ __global__ __launch_bounds__(64 * WQ * WT) void kv_prefix_kernel(KvAttnArgs a) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < 3; ++k)
 #pragma unroll
         for (int j = 0; j < 8; ++j) part[h][k][j] = (__bf16)((float)part[h][k][j] * f);
   };
@@ -253,7 +255,7 @@ __global__ __launch_bounds__(64 * WQ * WT) void kv_prefix_kernel(KvAttnArgs a) {
       for (int t = 0; t < DP / 32; ++t) {
         const bf16x8 f = read_v(v, h, t);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) acc[t] = mfma32(f, part[h][k], acc[t]);
+        for (int k = 0; k < 3; ++k) acc[t] = mfma32(f, part[h][k], acc[t]);
       }
   };
   auto products = [&](const __bf16* k) {
@@ -305,7 +307,7 @@ __global__ __launch_bounds__(64 * WQ * WT) void kv_prefix_kernel(KvAttnArgs a) {
         float w[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[j] = x[8 * h + j];
-        split2<!CODED>(w, part[h]);
+        split<!CODED>(w, part[h]);
       }
       float top;
       scores(sc, lds.ks[kb] + next, &top);
@@ -313,7 +315,7 @@ __global__ __launch_bounds__(64 * WQ * WT) void kv_prefix_kernel(KvAttnArgs a) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) asm volatile("" : "+v"(part[h][k]));
+        for (int k = 0; k < 3; ++k) asm volatile("" : "+v"(part[h][k]));
       settle(whole(kb, next), lds.bias[kb] + next, top);
     }
     nk ^= 1;

@@ -334,7 +334,7 @@ __global__ __launch_bounds__(64 * W) void paged_attention_kernel(AttnArgs a, int
       l += p[j];
     }
     bf16x8 part[3];
-    split(p, part);
+    split<true>(p, part);
     lds_in_order();
 #pragma unroll
     for (int i = 0; i < DP / 16; ++i) {

@@ -57,11 +57,14 @@ __device__ __forceinline__ bf16x8 upper(const uint32_t (&w)[8]) {
   v.w = __builtin_amdgcn_perm(w[7], w[6], 0x07060302u);
   return __builtin_bit_cast(bf16x8, v);
 }
-// Weights p as sums of three bfloat16 numbers each, exactly.  A part is the
-// bfloat16 number next below what is left, so a remainder is never zero: 16 bits
-// at most are left after the first and 8 after the second, or the one bit that
+
+// Weights p as sums of three bfloat16 numbers each, exactly: cut off after 8 bits,
+// and what is left again.  INF: for values that may be infinities.  A part is then
+// the bfloat16 number next below what is left, so a remainder is never zero: 16
+// bits at most are left after the first and 8 after the second, or the one bit that
 // was between neighbours.  All parts are positive (zero for a weight of zero), so
 // an infinity of V stays what it is in all three products.
+template <bool INF>
 __device__ __forceinline__ void split(const float (&p)[8], bf16x8 (&part)[3]) {
   uint32_t w[8];
   float left[8];
@@ -71,7 +74,9 @@ __device__ __forceinline__ void split(const float (&p)[8], bf16x8 (&part)[3]) {
   for (int k = 0; k < 2; ++k) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      w[j] = __builtin_elementwise_sub_sat(__float_as_uint(left[j]), 1u) & 0xFFFF0000u;
+      w[j] = __float_as_uint(left[j]);
+      if (INF) w[j] = __builtin_elementwise_sub_sat(w[j], 1u);
+      w[j] &= 0xFFFF0000u;
       left[j] -= __uint_as_float(w[j]);
     }
     part[k] = upper(w);
@@ -79,24 +84,6 @@ __device__ __forceinline__ void split(const float (&p)[8], bf16x8 (&part)[3]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(left[j]);
   part[2] = upper(w);
-}
-
-// The same in two parts: the second is rounded, so 16 bits stay at least (2^-8 of
-// a remainder under 2^-7).  INF: as above, no part is zero where the weight is not;
-// else the first is the weight cut off.
-template <bool INF>
-__device__ __forceinline__ void split2(const float (&p)[8], bf16x8 (&part)[2]) {
-  uint32_t w[8];
-  float left[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    w[j] = INF ? __builtin_elementwise_sub_sat(__float_as_uint(p[j]), 1u) : __float_as_uint(p[j]);
-    w[j] &= 0xFFFF0000u;
-    left[j] = p[j] - __uint_as_float(w[j]);
-  }
-  part[0] = upper(w);
-  part[1] = __builtin_bit_cast(bf16x8, make_uint4(pack_bf2(left[0], left[1]), pack_bf2(left[2], left[3]),
-                                                  pack_bf2(left[4], left[5]), pack_bf2(left[6], left[7])));
 }
 
 }  // namespace qlora

@@ -204,8 +204,12 @@ __global__ __launch_bounds__(64 * WQ * WT) void kv_prefix_kernel(KvAttnArgs a) {
     for (int j = 0; j < 16; ++j) t = fmaxf(t, x[j]);
     *top = t;
   };
-  // What is seldom: tokens that are not there, and a larger maximum.  m stays
-  // while no weight passes 2^8, which takes nothing from their precision.
+  // What is seldom: tokens that are not there, and a larger maximum.  m is set kAhead
+  // beyond it, so that it stays while the maximum grows less than that: no weight
+  // passes 1, so none times a value passes what the narrow workgroups can hold, and
+  // the largest is 2^-kAhead at least, far from where numbers end below (64 sequences
+  // behind 16384 tokens: 77 us, with 4 for kAhead 79, with 2 84, with 0 92).
+  constexpr float kAhead = 8.0f;
   auto settle = [&](int ok, const float* bias, float top) {
     if (!__builtin_amdgcn_readfirstlane(ok)) {
       top = -INFINITY;
@@ -219,11 +223,11 @@ __global__ __launch_bounds__(64 * WQ * WT) void kv_prefix_kernel(KvAttnArgs a) {
         }
       }
     }
-    if (!__ballot(top > 8.0f || m == -INFINITY)) return;
+    if (!__ballot(top > 0.0f || m == -INFINITY)) return;
     top = fmaxf(top, __shfl_xor(top, 32, 64));
-    const bool up = top > 8.0f || (m == -INFINITY && top > -INFINITY);
+    const bool up = top > 0.0f || (m == -INFINITY && top > -INFINITY);
     if (!__ballot(up)) return;
-    const float by = up ? ceilf(top) : 0.0f;  // m moves by it
+    const float by = up ? ceilf(top) + kAhead : 0.0f;  // m moves by it
     const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(-by);
     if (up) m = (m == -INFINITY ? 0.0f : m) + by;
     l *= f;

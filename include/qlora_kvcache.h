@@ -97,7 +97,9 @@ int qlora_kv_read(const qlora_kv_cache* cache, const int32_t* slots, int64_t T, 
  * of one new token per sequence over the numbers that its cached rows stand for.
  * The arguments are those of qlora_paged_attention.  Codes enter the products
  * as they are (bf16 holds them exactly), a key's scale is put on its score, a
- * value's on its weight, in fp32.
+ * value's on its weight, in fp32, and the weight enters the product with V with all
+ * of its 24 bits, whatever the sizes of the call (with less where it is under 2^-109,
+ * so where a value's scale is under 2^-100 or so).
  */
 int qlora_kv_attention_workspace(const qlora_kv_cache* cache, int64_t S, int32_t q_heads, int64_t table_cols,
                                  int64_t* ws_bytes);

@@ -90,3 +90,32 @@ def test_weights_enter_with_all_their_bits(K, path):
     want = (p[:rows, None] - p[None, :]) / (p[:rows, None] + 3)
     assert ((out - want).abs() <= 2.0 ** -8 * want.abs() + 40 * U).all()
     assert math.isfinite(float(out.abs().max())) and float(out.abs().max()) > 0.05
+
+
+@pytest.mark.parametrize("size", [1.5 * 2.0 ** 126, 1.0, 2.0 ** -95])
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("path,S,d", [("own", 3, 64), ("few", 8, 64), ("many", 12, 64), ("many", 70, 128), ("many", 12, 256)])
+def test_values_of_any_size(K, path, S, d, kind, size):
+    """A token late in the line weighs 2^7 times as much as those before it: its weight
+    times its value must not pass the largest number on the way, nor lose bits below
+    the smallest normal one.  Weights are off by 16 u, the 128 sums by 2 u each; the
+    output is rounded by 2^-8 at most."""
+    n, late = 128, 69
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k = torch.zeros(n, 1, d, dtype=BF, device="cuda")
+    k[late, 0, 0] = 7.0
+    v = torch.randn(n, 1, d, generator=g, device="cuda") * 2.0 ** -9
+    v[late] = torch.where(v[late] < 0, -1.0, 1.0)
+    v = (v.double() * size).to(BF)
+    c = K.KVCache.zeros(n // 16, 1, 16, d, KINDS[kind])
+    K.qlora_kv_write(None, k, v, None, None, torch.arange(n, dtype=torch.int32, device="cuda"), c)
+    q = torch.zeros(S, 4, d, dtype=BF, device="cuda")
+    q[..., 0] = 1.0
+    got = _attend(K, path, q, c, n, scale=math.log(2.0)).double()
+    values = c.v.double() if kind == "bf16" else c.v.float().double() * c.v_scale.double()[..., None]
+    values = values[:, 0].reshape(n, d)
+    p = torch.ones(n, dtype=torch.float64, device="cuda")
+    p[late] = 2.0 ** 7
+    want, wt = p @ values / p.sum(), p @ values.abs() / p.sum()
+    assert torch.isfinite(want).all() and (want.abs() > 0.4 * size).all()
+    assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + 272 * U * wt).all()

@@ -314,7 +314,7 @@ __global__ __launch_bounds__(64 * W, DP > 128 ? 1 : 2) void kv_attention_kernel(
       if constexpr (kCoded<CT>) p[j] *= vs[j];
     }
     bf16x8 part[3];
-    split<true>(p, part);
+    split<!kCoded<CT>>(p, part);
     lds_in_order();
 #pragma unroll
     for (int i = 0; i < DP / 16; ++i) {

@@ -59,7 +59,8 @@ __device__ __forceinline__ bf16x8 upper(const uint32_t (&w)[8]) {
 }
 
 // Weights p as sums of three bfloat16 numbers each, exactly: cut off after 8 bits,
-// and what is left again.  INF: for values that may be infinities.  A part is then
+// and what is left again, for weights of either sign (codes with a scale of -0 or
+// below).  INF: for weights not below 0 and values that may be infinities.  A part is then
 // the bfloat16 number next below what is left, so a remainder is never zero: 16
 // bits at most are left after the first and 8 after the second, or the one bit that
 // was between neighbours.  All parts are positive (zero for a weight of zero), so

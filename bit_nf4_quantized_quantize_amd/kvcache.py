@@ -82,7 +82,8 @@ def native():
 class KVCache(collections.namedtuple("KVCache", "k v k_scale v_scale")):
     """The rows of one layer's paged cache: k and v [num_pages, kv_heads,
     page_size, head_dim], bfloat16, or int8 or float8_e4m3fn codes with k_scale and
-    v_scale float32 [num_pages, kv_heads, page_size] (None for bfloat16)."""
+    v_scale float32 [num_pages, kv_heads, page_size] (None for bfloat16): an element
+    is code * scale, the scale finite, or NaN for a row that could not be held."""
 
     __slots__ = ()
 

@@ -38,9 +38,10 @@ typedef enum {
  *   k, v       [num_pages, kv_heads, page_size, head_dim]: rotated keys and
  *              values, bf16 or codes.  Token slot s is row s % page_size of page
  *              s / page_size.
- *   k_scale, v_scale   fp32 [num_pages, kv_heads, page_size]: the rows' scales,
- *              not negative (NULL for BF16).  NaN marks a row that cannot be
- *              held: it reads as NaN throughout.
+ *   k_scale, v_scale   fp32 [num_pages, kv_heads, page_size]: the rows' scales
+ *              (NULL for BF16), finite; qlora_kv_write makes none below 0, but any
+ *              may be.  NaN marks a row that cannot be held: it reads as NaN
+ *              throughout.
  *   page_size  a power of two, 1 .. 1024 (16 .. 1024 for the attention);
  *              num_pages * page_size < 2^31.
  *   head_dim   up to 256, a multiple of 16 (of 8 for BF16).

@@ -119,3 +119,36 @@ def test_values_of_any_size(K, path, S, d, kind, size):
     want, wt = p @ values / p.sum(), p @ values.abs() / p.sum()
     assert torch.isfinite(want).all() and (want.abs() > 0.4 * size).all()
     assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + 272 * U * wt).all()
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("path", PATHS)
+def test_scales_of_either_sign(K, path, kind):
+    """A row's numbers are code times scale, also for a scale of -0 or below it, and
+    for a weight of 0.  Tolerance: a score's products and their sum are off by 2 (d + 8)
+    u of their sizes' sum, the weight by that and 16 u more, 48 sums by 2 u each; the
+    output is rounded by 2^-8.  A weight under 2^-126 of the largest is no normal fp32
+    number and may count as nothing: where one token has all the weight and a value of
+    0 the result is made of such ones alone."""
+    n, KV, d, S = 48, 2, 64, _sequences(path, 20)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    c = K.KVCache.zeros(n // 16, KV, 16, d, KINDS[kind])
+    z = [torch.randn(n, KV, d, generator=g, device="cuda").to(BF) for _ in "kv"]
+    K.qlora_kv_write(None, *z, None, None, torch.arange(n, dtype=torch.int32, device="cuda"), c)
+    for t in (c.k_scale, c.v_scale):
+        t[:, :, 3::5] *= -1.0
+    c.v_scale[:, :, 4::6], c.k_scale[1, :, 2] = -0.0, -0.0
+    c.k_scale[2, 0, 5] *= 400.0           # one token takes all of a row's weight, or none of it
+    q = torch.randn(S, 4, d, generator=g, device="cuda").to(BF)
+    got = _attend(K, path, q, c, n).double()
+    k, v = ((t.float().double() * s.double()[..., None]).transpose(1, 2).reshape(n, KV, d)
+            for t, s in ((c.k, c.k_scale), (c.v, c.v_scale)))
+    for h in range(4):
+        score = q[:, h].double() @ k[:, h // 2].t().contiguous() / math.sqrt(d)
+        p = torch.softmax(score, -1)
+        want, wt = p @ v[:, h // 2], p @ v[:, h // 2].abs()
+        size = (q[:, h].double().abs() @ k[:, h // 2].abs().t().contiguous()).amax(-1, keepdim=True) / math.sqrt(d)
+        e = (2 * (d + 8) + 16) * U * (1 + size)
+        assert ((got[:, h] - want).abs() <= 2.0 ** -8 * want.abs() + (2 * e + 112 * U) * wt +
+                n * 2.0 ** -126 * float(v.abs().max())).all(), h
+    assert (q[:, 0].double() @ k[:, 0].t().contiguous()).abs().max() / 8 > 100

@@ -499,11 +499,18 @@ static int wide_rows(int64_t rows, const KvCache& c, int64_t prefix_cols) {
 }
 constexpr int kWideWaves = 2;  // a part of the prefix has the tiles of that many narrow waves at least
 
-// The own tokens' parts as without a prefix; whole behind one of many rows if there
-// are enough workgroups, which then can join the prefix's parts (64 sequences of 100
-// to 800, 64 on 8 heads: 26 us, against 23 and 11 for the join; finer parts, for the
-// join, do not pay: 256 of 0 to 700 in parts of 256 tokens 52 us, whole 50).  The
-// prefix's: a workgroup per CU, as far as its length gives each some tiles (16 rows
+// Own tokens stay whole up to that many of them, so that their workgroups can join
+// the prefix's parts.
+constexpr int64_t kWholeOwn = 1024;
+
+// The own tokens' parts as without a prefix; but whole where their workgroups then
+// join the prefix's parts (launch_kv_attention), if these are enough and lengths
+// end at kWholeOwn (64 sequences of 100 to 800, 64 on 8 heads: 26 us, against 23 and
+// 11 for the join; finer parts, for the join, do not pay: 256 of 0 to 700 in parts
+// of 256 tokens 52 us, whole 50).  Behind 8000 tokens, 64 sequences of 1 to 1024, 32
+// on 8 heads, int8: whole 57 us, cut 63; of 1 to 2048 75 and 74; 32 of 1 to 16384
+// 270 and 164, one of 16384 among 31 of 256 262 and 95.
+// The prefix's: a workgroup per CU, as far as its length gives each some tiles (16 rows
 // of 8191 tokens, 32 heads: 41 us so, 45 with two, 49 with four).
 KvParts kv_parts(const KvCache& c, int64_t S, int q_heads, int64_t table_cols, int64_t prefix_cols) {
   KvParts p;
@@ -514,7 +521,9 @@ KvParts kv_parts(const KvCache& c, int64_t S, int q_heads, int64_t table_cols, i
   const int64_t rows = S * (q_heads / c.kv_heads), cap = prefix_cols << c.page_shift;
   const int wide = wide_rows(rows, c, prefix_cols);
   const int64_t groups = c.kv_heads * (wide ? (rows + wide - 1) / wide : (rows + 15) / 16);
-  if (wide && S * c.kv_heads * ((q_heads / c.kv_heads + 15) / 16) >= 256) p.own = 1;
+  if (wide && q_heads > c.kv_heads && max_len <= kWholeOwn &&
+      S * c.kv_heads * ((q_heads / c.kv_heads + 15) / 16) >= 256)
+    p.own = 1;
   int64_t n = (256 + groups - 1) / groups;
   const int64_t least = (wide ? kWideWaves : 4) * kMinTiles * kTile, most = (cap + least - 1) / least;
   if (n > most) n = most;

@@ -213,16 +213,18 @@ class PagedCache:
         self.host_lens = [0] * max_seqs
         self.prefix_table = torch.full((-(-self.max_prefix // page_size),), -1, dtype=torch.int32, device=dev)
         self.prefix_len = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.prefix_slots = torch.zeros(0, dtype=torch.int32, device=dev)
+        self.prefix_pages, self.prefix_slots = self.prefix_table[:0], torch.zeros(0, dtype=torch.int32, device=dev)
         self.host_prefix = 0
         self.used = 0
 
     def state(self):
         """What the cache counts; set_state takes it back to that."""
-        return self.lens, self.host_lens, self.prefix_len, self.prefix_slots, self.host_prefix, self.used
+        return (self.lens, self.host_lens, self.prefix_len, self.prefix_pages, self.prefix_slots, self.host_prefix,
+                self.used)
 
     def set_state(self, state):
-        self.lens, self.host_lens, self.prefix_len, self.prefix_slots, self.host_prefix, self.used = state
+        (self.lens, self.host_lens, self.prefix_len, self.prefix_pages, self.prefix_slots, self.host_prefix,
+         self.used) = state
 
     def _take(self, need):
         """Refuses what cannot be had before anything is enqueued."""
@@ -263,6 +265,8 @@ class PagedCache:
                                   torch.tensor([n], dtype=torch.int32).to(dev), self.free[self.used:],
                                   self.prefix_table[None], self.page_size, n)
         self.prefix_len, self.prefix_slots, self.host_prefix = plan.total_lens, plan.slots, int(n)
+        # the kernels are chosen by the room of the table they are given
+        self.prefix_pages = self.prefix_table[:need]
         self.used += need
         return plan
 
@@ -447,7 +451,7 @@ class QLoraBlock:
         def attend(plan, q, k, v):
             q = K.qlora_kv_write(q, k, v, self.rope, self._behind(plan.positions, cache), plan.slots, cache.rows)
             if cache.host_prefix:
-                o = K.qlora_prefix_attention(q, cache.rows, cache.prefix_table, cache.prefix_len, cache.table, cache.lens)
+                o = K.qlora_prefix_attention(q, cache.rows, cache.prefix_pages, cache.prefix_len, cache.table, cache.lens)
             elif cache.rows.k_scale is not None:
                 o = K.qlora_kv_attention(q, cache.rows, cache.table, cache.lens)
             else:

@@ -275,10 +275,16 @@ def rms_norm(z, g):
     return z * torch.rsqrt(torch.mean(z * z, dim=-1, keepdim=True) + EPS) * g
 
 
+# Scores that a call without gradients has in memory at a time (with their masked,
+# exponential and weighted copies some 5 GB).
+MOST_SCORES = 2 ** 28
+
+
 def causal_attention(q, k, v, heads, prefix=None):
     """softmax(q k^T / sqrt(d)) v per sequence and head, causal; fp32.
     q, k, v: [batch, seq, hidden]. prefix: keys and values [tokens, heads, d]
-    that come before every sequence."""
+    that come before every sequence. Where no gradient is wanted and the scores are
+    more than MOST_SCORES, sequences or rows of one are taken in turns."""
     b, t, hd = q.shape
     d = hd // heads
 
@@ -286,16 +292,35 @@ def causal_attention(q, k, v, heads, prefix=None):
         return z.reshape(b, t, heads, d).permute(0, 2, 1, 3).contiguous()
 
     qh, kh, vh = split(q), split(k), split(v)
-    scores = torch.matmul(qh, kh.transpose(-1, -2).contiguous()) / math.sqrt(d)
-    future = torch.triu(torch.ones(t, t, dtype=torch.bool, device=q.device), diagonal=1)
-    scores = scores.masked_fill(future, float("-inf"))
-    if prefix is None:
-        return torch.matmul(torch.softmax(scores, dim=-1), vh).permute(0, 2, 1, 3).reshape(b, t, hd)
-    pk, pv = (z.float().transpose(0, 1).contiguous() for z in prefix)
-    before = torch.matmul(qh, pk.transpose(-1, -2).contiguous()) / math.sqrt(d)
-    p = torch.softmax(torch.cat((before, scores), -1), dim=-1)
-    n = pk.shape[1]
-    o = torch.matmul(p[..., :n].contiguous(), pv) + torch.matmul(p[..., n:].contiguous(), vh)
+    if prefix is not None:
+        pk, pv = (z.float().transpose(0, 1).contiguous() for z in prefix)
+        pk = pk.transpose(-1, -2).contiguous()
+
+    def rows(qr, first, kt, vr):
+        """The rows from the first one on, over the keys up to their last."""
+        scores = torch.matmul(qr, kt) / math.sqrt(d)
+        future = torch.triu(torch.ones(scores.shape[-2:], dtype=torch.bool, device=q.device), diagonal=1 + first)
+        scores = scores.masked_fill(future, float("-inf"))
+        if prefix is None:
+            return torch.matmul(torch.softmax(scores, dim=-1), vr)
+        before = torch.matmul(qr, pk) / math.sqrt(d)
+        p = torch.softmax(torch.cat((before, scores), -1), dim=-1)
+        n = pv.shape[1]
+        return torch.matmul(p[..., :n].contiguous(), pv) + torch.matmul(p[..., n:].contiguous(), vr)
+
+    of_row = heads * (t + (0 if prefix is None else pv.shape[1]))
+    if torch.is_grad_enabled() or b * t * of_row <= MOST_SCORES:
+        o = rows(qh, 0, kh.transpose(-1, -2).contiguous(), vh)
+    else:
+        # whole sequences as far as they fit, else rows of one
+        o, step = torch.empty_like(qh), max(1, min(t, MOST_SCORES // of_row))
+        seqs = max(1, MOST_SCORES // (t * of_row))
+        for s in range(0, b, seqs):
+            qs, ks, vs = (z[s:s + seqs] for z in (qh, kh, vh))
+            for i in range(0, t, step):
+                j = min(i + step, t)
+                o[s:s + seqs, :, i:j] = rows(qs[:, :, i:j].contiguous(), i,
+                                             ks[:, :, :j].transpose(-1, -2).contiguous(), vs[:, :, :j].contiguous())
     return o.permute(0, 2, 1, 3).reshape(b, t, hd)
 
 

@@ -488,10 +488,11 @@ int waves_for(const KvAttnArgs& a) {
 
 // Rows of a prefix's workgroup: narrow ones (0) up to 32, and as long as they read
 // little in all, in the launch of the own tokens instead of one before it (128 rows,
-// 8 kv heads, int8, 1000 tokens 19 us, wide 26; 4000, at the limit, 31 and 32; 8000
-// 46 and 36).  1024 rows at most, so that a grid holds them.  Wide ones of 128 up
-// to 256 rows (256 of 8 kv heads, 2000 tokens 31 us, with 256 34; 16000 56 and 59;
-// 512 of 16000 87 and 82).
+// 8 kv heads, int8, 1000 tokens 20 us, wide 27; 4000, at the limit, 31 and 33; 8000
+// 46 and 38; with 32 kv heads even at twice the limit or four times, 128 rows of 2000
+// 56 and 63, of 4000 76 and 73).  1024 rows at most, so that a grid holds them.  Wide
+// ones of 128 up to 256 rows (256 of 8 kv heads, 4000 tokens 37 us, with 256 42; 8000
+// 45 and 50; 512 of 16000 101 and 93).
 static int wide_rows(int64_t rows, const KvCache& c, int64_t prefix_cols) {
   const int64_t reads = ((rows + 15) / 16) * c.kv_heads * (prefix_cols << c.page_shift);
   if (rows <= 32 || (rows <= 1024 && reads <= 1 << 18)) return 0;
@@ -540,8 +541,8 @@ hipError_t launch_kv_attention(const KvAttnArgs& args, hipStream_t stream) {
   a.wide = a.psplits ? wide_rows(a.S * group, a.c, a.prefix_cols) : 0;
   a.pwaves = a.wide ? kWideWaves : a.waves;
   // A workgroup of one row would join it with a few of its threads only (behind 2000
-  // tokens, bf16, 256 sequences on 32 of 32 heads: joined 144 us, by the kernel below
-  // 115; 128 on 8 of 32: 43 and 46).
+  // tokens, bf16, 256 sequences on 32 of 32 heads: joined 148 us, by the kernel below
+  // 122; 128 on 8 of 32: 45 and 49).
   a.joined = a.wide && a.splits == 1 && group > 1;
   if (a.wide) {
     const hipError_t e = launch_kv_prefix(a, stream);

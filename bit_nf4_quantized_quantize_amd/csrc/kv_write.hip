@@ -75,10 +75,11 @@ __device__ __forceinline__ uint32_t exact_code(float x, const Scale& k) {
 
 // The codes of sixteen elements, in four words.  The quotient x * (1 / s) is off
 // by less than two steps of fp32, so its rounding is the nearest code unless it
-// lies that near to the middle of two; elements there (and quotients under the
-// smallest normal E4M3 number, whose middles lie elsewhere) are done over.  That
-// is one in 10^4 of ordinary rows; all elements done exactly took 91 us where this
-// takes 79 (8192 tokens of 32 heads of 128).
+// lies that near to the middle of two; a lane's elements are done over if one is there
+// (or under the smallest normal E4M3 number, whose middles lie elsewhere: zeros are).
+// That is one element in 10^4 of ordinary rows, so a wave in ten, of 1024 elements,
+// takes the longer way; all of them took 91 us where this takes 78 (8192 tokens of
+// 32 heads of 128; with one zero in 50 elements 80).
 template <int CT>
 __device__ __forceinline__ void codes_of(const float (&x)[16], const Scale& k, uint32_t (&w)[4]) {
   bool near = k.zero | (k.up != 1.0f);

@@ -67,8 +67,8 @@ typedef struct qlora_kv_cache {
  *     scale = a / M rounded to fp32,  M = 127 (INT8) or 448 (E4M3),
  *     code  = the one nearest to z / scale (that quotient exactly, ties to the
  *             even code), at most M in size;
- * a row of zeros has scale 0 and codes 0, a row that holds a NaN or an infinity
- * scale NaN and codes 0.
+ * a row of zeros has scale 0 and codes 0 (as has one whose scale rounds to 0), a row
+ * that holds a NaN or an infinity scale NaN and codes 0.
  *
  *   q, qo, k, v, positions, turns, mscale, interleaved, slots, strides: as for
  *              qlora_rope_cache_write (bf16).  No two tokens may have the same

@@ -100,7 +100,9 @@ int qlora_kv_read(const qlora_kv_cache* cache, const int32_t* slots, int64_t T, 
  * as they are (bf16 holds them exactly), a key's scale is put on its score, a
  * value's on its weight, in fp32, and the weight enters the product with V with all
  * of its 24 bits, whatever the sizes of the call (with less where it is under 2^-109,
- * so where a value's scale is under 2^-100 or so).
+ * so where a value's scale is under 2^-100 or so).  Weights are exp of the score less
+ * the row's largest, at most 1; the sum of the values they weigh has to stay in the
+ * range of fp32 before it is divided by theirs.
  */
 int qlora_kv_attention_workspace(const qlora_kv_cache* cache, int64_t S, int32_t q_heads, int64_t table_cols,
                                  int64_t* ws_bytes);
